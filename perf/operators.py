@@ -1,0 +1,379 @@
+"""The paged key/value cache and the attention that reads it: cases, plain forms and exact values.
+
+Between the fused QKV projection (q [Hq, M, D], k and v [Hkv, M, D], head-major) and the output projection
+(a [M, Hq * D]) a decoder layer does two things, and a prompt's keys and values are sometimes read back:
+
+  append     q and k are rotated by their positions, k and v are written into the sequences' pages
+             (bf16 pages, or 4-bit pages with one scale and one minimum per token and head)
+  attention  softmax(scale q k^T) v over the pages, causal, optionally with a sliding window and a few
+             first tokens that stay visible (sinks); one token per sequence, or many
+  gather     the tokens of a batch read back from their pages as bf16 (the values 4-bit pages stand for)
+
+A batch is described the way a serving loop holds it: cu_q [B + 1] (rows of each sequence's new tokens in the
+packed batch), kv_len [B] (tokens of each sequence in the cache, the new ones included), block_table [B, P].
+Token i of sequence b's n new ones has position kv_len[b] - n + i.
+
+4-bit pages: x (bf16) of one token and head is stored as lo = min x, s = (max x - lo) / 15 rounded up to bf16,
+code = round((x - lo) / s) (0 where s is 0), two codes a byte, the lower d in the low nibble; it stands for
+lo + code * s.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda"
+
+
+# ------------------------------------------------------------------------------------------------ cases
+def _case(name, op, fmt="bf16", Hq=32, Hkv=8, D=128, page=64, B=1, new=(1, 1), ctx=(0, 0), window=0, sinks=0,
+          rot=0, interleaved=False, lse=False, lens_seed=1):
+    c = dict(op=op, fmt=fmt, Hq=Hq, Hkv=Hkv, D=D, page=page, B=B, new_lo=new[0], new_hi=new[1], ctx_lo=ctx[0],
+             ctx_hi=ctx[1], window=window, sinks=sinks, rot=rot, interleaved=interleaved, lse=lse,
+             lens_seed=lens_seed)
+    if name is not None:
+        c["name"] = name
+    return c
+
+
+def listed():
+    return [
+        # one token of one sequence, the small head layout of the tiny workload: launch latency
+        _case("append_one_token", "append", Hq=4, Hkv=2, D=64, page=16, ctx=(37, 37), rot=64),
+        # a decode step of 64 sequences with the 70B heads into 4-bit pages; read back as the values they stand for
+        _case("append_decode_int4", "append", fmt="int4", Hq=64, Hkv=8, page=128, B=64, ctx=(5, 4000), rot=128),
+        # the packed prompt batch: 64 ragged prompts with the 70B heads, interleaved pairs, half of each head rotated
+        _case("append_prompts", "append", Hq=64, Hkv=8, page=128, B=64, new=(1, 2048), rot=64, interleaved=True),
+        # a prompt batch with the 8B heads into 4-bit pages
+        _case("append_prompts_int4", "append", fmt="int4", Hq=32, Hkv=8, page=64, B=13, new=(700, 2048), rot=128),
+        # one sequence, one token, a few hundred behind it: latency
+        _case("attend_one_sequence", "attend", Hq=32, Hkv=8, page=16, ctx=(500, 500)),
+        # a decode step of 32 ragged sequences, 70B heads
+        _case("attend_decode", "attend", Hq=64, Hkv=8, page=128, B=32, ctx=(300, 8191)),
+        # long streams held to a window and four sinks; the log-sum-exp for joining with another cache's part
+        _case("attend_decode_window", "attend", Hq=32, Hkv=8, page=32, B=24, ctx=(9000, 60000), window=4096, sinks=4,
+              lse=True),
+        # ragged prompts, 8B heads, nothing cached before
+        _case("attend_prompts", "attend", Hq=32, Hkv=8, page=64, B=4, new=(900, 4096)),
+        # a chunk of a long prompt, 70B heads, on what the earlier chunks left
+        _case("attend_chunk", "attend", Hq=64, Hkv=8, page=128, new=(2048, 2048), ctx=(22001, 22001)),
+        # a decode step of 64 ragged sequences over 4-bit pages, 8B heads
+        _case("attend_decode_int4", "attend", fmt="int4", Hq=32, Hkv=8, page=64, B=64, ctx=(2000, 12000)),
+        # one long sequence over 4-bit pages, 70B heads, two tokens at once (one of them a draft)
+        _case("attend_long_int4", "attend", fmt="int4", Hq=64, Hkv=8, page=128, new=(2, 2), ctx=(130001, 130001)),
+        # prompts continued over 4-bit pages, a smaller head
+        _case("attend_chunk_int4", "attend", fmt="int4", Hq=16, Hkv=4, D=64, page=32, B=5, new=(100, 900),
+              ctx=(0, 3000), window=2000, sinks=8),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    fmt = rng.choice(["bf16", "int4"])
+    D = rng.choice([64, 128, 128])
+    page = rng.choice([16, 32, 64, 128])
+    Hkv = rng.choice([1, 2, 4, 8])
+    Hq = Hkv * rng.choice([1, 2, 3, 4, 7, 8])
+    seed = rng.randrange(1 << 20)
+    kind = rng.choice(["append", "decode", "decode", "many"])
+    if kind == "append":
+        B = _log(rng, 1, 64)
+        hi = _log(rng, 1, 2000)
+        rot = rng.choice([0, D // 2, D, D])
+        return _case(None, "append", fmt, Hq, Hkv, D, page, B, (max(1, hi // 3), hi), (0, _log(rng, 1, 4000)),
+                     rot=rot, interleaved=rng.random() < 0.5, lens_seed=seed)
+    window = rng.choice([0, 0, _log(rng, 16, 4096)])
+    sinks = rng.choice([0, rng.randrange(1, 40)]) if window else 0
+    if kind == "decode":
+        B = _log(rng, 1, 64)
+        hi = _log(rng, 1, min(130000, 500000 // B))
+        return _case(None, "attend", fmt, Hq, Hkv, D, page, B, (1, rng.choice([1, 1, 2])), (hi // 4, hi), window,
+                     sinks, lse=rng.random() < 0.3, lens_seed=seed)
+    B = _log(rng, 1, 8)
+    hi = _log(rng, 3, 4096 // B)
+    return _case(None, "attend", fmt, min(Hq, 32), Hkv, D, page, B, (max(1, hi // 3), hi), (0, _log(rng, 1, 4000)),
+                 window, sinks, lse=rng.random() < 0.3, lens_seed=seed)
+
+
+def _lengths(c):
+    """(new tokens, cached tokens before them) of each sequence: numpy int64 [B] each, of the case alone."""
+    r = np.random.default_rng(c["lens_seed"])
+    return (r.integers(c["new_lo"], c["new_hi"] + 1, c["B"]), r.integers(c["ctx_lo"], c["ctx_hi"] + 1, c["B"]))
+
+
+# ------------------------------------------------------------------------------------------------ inputs
+def _pack_rows(x):
+    """bf16 rows [..., D] -> (codes uint8 [..., D / 2], scale and minimum bf16 [..., 2])."""
+    f = x.float()
+    lo, hi = f.amin(-1, keepdim=True), f.amax(-1, keepdim=True)
+    s = (hi - lo) / torch.tensor(15.0, device=f.device)
+    s = ((s.view(torch.int32) + 0xFFFF) & -0x10000).view(torch.float32)     # the next bf16 at or above it
+    c = torch.where(s > 0, torch.round((f - lo) / torch.where(s > 0, s, torch.ones_like(s))), torch.zeros_like(f))
+    c = c.clamp_(0, 15).to(torch.uint8)
+    return c[..., 0::2] | (c[..., 1::2] << 4), torch.cat([s, lo], -1).to(torch.bfloat16)
+
+
+def _unpack_rows(codes, sl):
+    """What 4-bit rows stand for, fp32 [..., D]."""
+    c = torch.stack([codes & 15, codes >> 4], -1).flatten(-2).float()
+    sl = sl.float()
+    return sl[..., 1:2] + c * sl[..., 0:1]
+
+
+def prepare(case, seed):
+    c = case
+    new, ctx = _lengths(c)
+    B, page, Hq, Hkv, D = c["B"], c["page"], c["Hq"], c["Hkv"], c["D"]
+    M = int(new.sum())
+    kv = new + ctx
+    n_pages = -(-kv // page)
+    P = int(n_pages.max())
+    r = np.random.default_rng(seed)
+    pool = int(n_pages.sum()) + 3
+    order = r.permutation(pool)
+    table = np.zeros((B, P), np.int32)
+    at = np.concatenate([[0], np.cumsum(n_pages)])
+    for b in range(B):
+        table[b, :n_pages[b]] = order[at[b]:at[b + 1]]
+    g = torch.Generator(DEV).manual_seed(int(seed))
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device=DEV, dtype=torch.bfloat16)
+
+    s = {"case": c, "M": M, "max_q": int(new.max()),
+         "cu_q": torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device=DEV),
+         "kv_len": torch.tensor(kv, dtype=torch.int32, device=DEV),
+         "table": torch.tensor(table, device=DEV),
+         "scale": 1.0 / math.sqrt(D), "q": normal(Hq, M, D)}
+    rows = (pool, Hkv, page)
+    if c["op"] == "append":
+        s["k"], s["v"] = normal(Hkv, M, D), normal(Hkv, M, D)
+        if c["rot"]:
+            inv = 500000.0 ** (-torch.arange(0, c["rot"], 2, dtype=torch.float64, device=DEV) / c["rot"])
+            ang = torch.arange(int(kv.max()), dtype=torch.float64, device=DEV)[:, None] * inv
+            s["cos"], s["sin"] = ang.cos().float(), ang.sin().float()
+    for n in ("k", "v"):
+        pages = normal(*rows, D)
+        if c["fmt"] == "bf16":
+            s[n + "_pages"] = pages
+        else:
+            s[n + "_pages"] = torch.empty(*rows, D // 2, dtype=torch.uint8, device=DEV)
+            s[n + "_scale"] = torch.empty(*rows, 2, dtype=torch.bfloat16, device=DEV)
+            for i in range(0, pool, 512):
+                s[n + "_pages"][i:i + 512], s[n + "_scale"][i:i + 512] = _pack_rows(pages[i:i + 512])
+        del pages
+    if own:    # what a serving program keeps between calls: the handle, the cache and the batch's description
+        from transformer_layer_residual_b200 import fnl
+        s["handle"] = fnl.Handle(0)
+        s["cache"] = fnl.KVCache(s["k_pages"], s["v_pages"], s.get("k_scale"), s.get("v_scale"))
+        s["batch"] = fnl.KVBatch(s["cu_q"], s["kv_len"], s["table"], s["max_q"])
+    return s
+
+
+# ------------------------------------------------------------------------------------------------ runs
+def _rotate(x, cos, sin, rot, interleaved):
+    """Rotation of the first `rot` of each head's D values; cos and sin fp32 [M, rot / 2]."""
+    f = x.float()
+    if interleaved:
+        a, b = f[..., 0:rot:2], f[..., 1:rot:2]
+        y = torch.stack([a * cos - b * sin, b * cos + a * sin], -1).flatten(-2)
+    else:
+        a, b = f[..., :rot // 2], f[..., rot // 2:rot]
+        y = torch.cat([a * cos - b * sin, b * cos + a * sin], -1)
+    return torch.cat([y, f[..., rot:]], -1).to(torch.bfloat16)
+
+
+def _token_rows(s):
+    """Of each packed token: its sequence, its index among the new ones, its position."""
+    t = torch.arange(s["M"], device=DEV, dtype=torch.int32)
+    b = torch.searchsorted(s["cu_q"], t, right=True) - 1
+    i = t - s["cu_q"][b]
+    return b, i, s["kv_len"][b] - (s["cu_q"][b + 1] - s["cu_q"][b]) + i
+
+
+def _append_plain(s):
+    c = s["case"]
+    b, i, pos = _token_rows(s)
+    q, k, v = s["q"], s["k"], s["v"]
+    if c["rot"]:
+        cos, sin = s["cos"][pos], s["sin"][pos]
+        q = _rotate(q, cos, sin, c["rot"], c["interleaved"])
+        k = _rotate(k, cos, sin, c["rot"], c["interleaved"])
+    page, off = s["table"][b, pos // c["page"]].long(), (pos % c["page"]).long()
+    if c["fmt"] == "bf16":
+        s["k_pages"][page, :, off] = k.transpose(0, 1)
+        s["v_pages"][page, :, off] = v.transpose(0, 1)
+        return {"q": q, "k_pages": s["k_pages"], "v_pages": s["v_pages"]}
+    out = {"q": q}
+    out.update({n: _store_int4(s, n, x, page, off) for n, x in (("k", k), ("v", v))})
+    return out
+
+
+def _store_int4(s, n, x, page, off):
+    codes, sl = _pack_rows(x)
+    s[n + "_pages"][page, :, off] = codes.transpose(0, 1)
+    s[n + "_scale"][page, :, off] = sl.transpose(0, 1)
+    return _unpack_rows(s[n + "_pages"][page, :, off], s[n + "_scale"][page, :, off]).transpose(0, 1).to(torch.bfloat16)
+
+
+def _pages_plain(s, n):
+    """The sequences' keys or values, fp32 [B, Hkv, P * page, D]."""
+    at = s["table"].long()
+    x = s[n + "_pages"][at]
+    x = x.float() if s["case"]["fmt"] == "bf16" else _unpack_rows(x, s[n + "_scale"][at])
+    return x.transpose(1, 2).flatten(2, 3)
+
+
+def _attend_plain(s):
+    c = s["case"]
+    B, Hq, Hkv, D, nq = c["B"], c["Hq"], c["Hkv"], c["D"], s["max_q"]
+    b, i, _ = _token_rows(s)
+    n = (s["cu_q"][1:] - s["cu_q"][:-1]).long()
+    step = torch.arange(nq, device=DEV)
+    at = torch.minimum(s["cu_q"][:-1].long()[:, None] + step, torch.tensor(s["M"] - 1, device=DEV))
+    q = s["q"].float()[:, at]                                              # [Hq, B, nq, D]
+    q = q.view(Hkv, Hq // Hkv, B, nq, D).permute(2, 0, 1, 3, 4).reshape(B, Hkv, -1, D)
+    k = _pages_plain(s, "k")
+    z = (q @ k.transpose(2, 3)).mul_(s["scale"])                           # [B, Hkv, group * nq, L]
+    del k, q
+    L = z.shape[3]
+    key = torch.arange(L, device=DEV)
+    pos = (s["kv_len"].long() - n)[:, None] + step                         # [B, nq]
+    seen = key <= pos[..., None]
+    if c["window"]:
+        seen &= (key > pos[..., None] - c["window"]) | (key < c["sinks"])
+    z = z.view(B, Hkv, Hq // Hkv, nq, L).masked_fill_(~seen[:, None, None], -math.inf)
+    top = z.amax(-1, keepdim=True)
+    z = z.sub_(top).exp_()
+    den = z.sum(-1, keepdim=True)
+    o = z.view(B, Hkv, -1, L) @ _pages_plain(s, "v")
+    o = o.view(B, Hkv, Hq // Hkv, nq, D).div_(den)
+    out = {"out": o[b, :, :, i].reshape(s["M"], Hq * D).to(torch.bfloat16)}
+    if c["lse"]:
+        out["lse"] = (top + den.log())[b, :, :, i, 0].reshape(s["M"], Hq).t().contiguous()
+    return out
+
+
+def run(state):
+    s, c = state, state["case"]
+    if not own:
+        return _append_plain(s) if c["op"] == "append" else _attend_plain(s)
+    from transformer_layer_residual_b200 import fnl
+    h = s["handle"]
+    if c["op"] == "append":
+        q = fnl.rope_append_kv(h, s["cache"], s["batch"], s["q"], s["k"], s["v"], s.get("cos"), s.get("sin"),
+                               interleaved=c["interleaved"])["q"]
+        if c["fmt"] == "bf16":
+            return {"q": q, "k_pages": s["k_pages"], "v_pages": s["v_pages"]}
+        back = fnl.kv_gather(h, s["cache"], s["batch"])
+        return {"q": q, "k": back["k"], "v": back["v"]}
+    lse = torch.empty(c["Hq"], s["M"], dtype=torch.float32, device=DEV) if c["lse"] else None
+    r = fnl.paged_attention(h, s["cache"], s["batch"], s["q"], scale=s["scale"], window=c["window"],
+                            sinks=c["sinks"], lse=lse)
+    return {"out": r["out"], "lse": lse} if c["lse"] else {"out": r["out"]}
+
+
+# ------------------------------------------------------------------------------------------------ work
+def work(case):
+    c = case
+    new, ctx = _lengths(c)
+    Hq, Hkv, D = c["Hq"], c["Hkv"], c["D"]
+    M = float(new.sum())
+    row = 2 * D if c["fmt"] == "bf16" else D // 2 + 4      # a token's keys (or values) of one head in the cache
+    lists = 4.0 * (2 * c["B"] + 1 + (-(-(new + ctx) // c["page"])).sum())
+    if c["op"] == "append":
+        b = M * 2 * D * (Hq + 2 * Hkv) + M * 2 * Hkv * row + lists
+        b += M * 2 * D * Hq if c["rot"] else 0
+        b += len({int(p) for n, x in zip(new, ctx) for p in range(x, x + n)}) * c["rot"] * 4.0
+        if c["fmt"] == "int4":
+            b += M * 2 * Hkv * (row + 2 * D)
+        return {"bytes": float(b), "flops": M * (Hq + Hkv) * c["rot"] * 3.0}
+    pairs, keys = 0.0, 0.0
+    for n, x in zip(new, ctx):
+        pos = np.arange(x, x + n)
+        lo = np.maximum(0, pos + 1 - c["window"]) if c["window"] else np.zeros_like(pos)
+        pairs += float((pos + 1 - lo + np.minimum(lo, c["sinks"])).sum())
+        keys += float(x + n - lo[0] + min(lo[0], c["sinks"]))
+    b = 2 * M * Hq * D * 2 + keys * Hkv * 2 * row + lists + (4 * M * Hq if c["lse"] else 0)
+    return {"bytes": float(b), "flops": 4.0 * pairs * Hq * D}
+
+
+# ------------------------------------------------------------------------------------------------ exact
+def _values64(s, n, b, h, length):
+    """Sequence b's stored keys or values of head h in 64 bits, [length, D]."""
+    page = s["case"]["page"]
+    ids = s["table"][b, :-(-length // page)].long()
+    x = s[n + "_pages"][ids, h].reshape(-1, s[n + "_pages"].shape[-1])[:length]
+    if s["case"]["fmt"] == "bf16":
+        return x.double()
+    sl = s[n + "_scale"][ids, h].reshape(-1, 2)[:length].double()
+    y = torch.empty(length, s["case"]["D"], dtype=torch.float64, device=DEV)
+    y[:, 0::2], y[:, 1::2] = (x % 16).double(), torch.div(x, 16, rounding_mode="floor").double()
+    return y * sl[:, :1] + sl[:, 1:]
+
+
+def _int4_64(x):
+    """The values that the 4-bit rows of bf16 x stand for, in 64 bits."""
+    x = x.double()
+    lo = x.min(-1, keepdim=True).values
+    s = (x.max(-1, keepdim=True).values - lo) / 15
+    near = s.to(torch.bfloat16)
+    up = torch.nextafter(near, torch.full_like(near, math.inf))
+    s = torch.where(near.double() < s, up, near).double()
+    code = torch.where(s > 0, ((x - lo) / s.clamp_min(1e-300)).round().clamp(0, 15), torch.zeros_like(x))
+    return lo + code * s
+
+
+def exact(case, seed):
+    c = case
+    if work(c)["flops"] > 4e12:
+        return None
+    s = prepare(c, seed)
+    new, ctx = _lengths(c)
+    Hq, Hkv, D, page = c["Hq"], c["Hkv"], c["D"], c["page"]
+    cu = [0] + [int(x) for x in np.cumsum(new)]
+    if c["op"] == "append":
+        pos = torch.tensor(np.concatenate([np.arange(x, x + n) for n, x in zip(new, ctx)]), device=DEV)
+        turned = {}
+        for n in ("q", "k"):
+            x = s[n].double()
+            if c["rot"]:
+                h = c["rot"] // 2
+                i = torch.arange(h, device=DEV)
+                one, two = (2 * i, 2 * i + 1) if c["interleaved"] else (i, i + h)
+                z = torch.complex(x[..., one], x[..., two]) * torch.complex(s["cos"].double(), s["sin"].double())[pos]
+                x[..., one], x[..., two] = z.real, z.imag
+            turned[n] = x
+        if c["fmt"] == "int4":
+            return {"q": turned["q"], "k": _int4_64(turned["k"].to(torch.bfloat16)), "v": _int4_64(s["v"])}
+        pages = {n: s[n + "_pages"].double() for n in ("k", "v")}
+        for n, x in (("k", turned["k"]), ("v", s["v"].double())):
+            for b in range(c["B"]):
+                p = pos[cu[b]:cu[b + 1]]
+                pages[n][s["table"][b].long()[p // page], :, p % page] = x[:, cu[b]:cu[b + 1]].transpose(0, 1)
+        return {"q": turned["q"], "k_pages": pages["k"], "v_pages": pages["v"]}
+    out = torch.zeros(s["M"], Hq, D, dtype=torch.float64, device=DEV)
+    lse = torch.zeros(Hq, s["M"], dtype=torch.float64, device=DEV)
+    for b in range(c["B"]):
+        n, L = int(new[b]), int(new[b] + ctx[b])
+        p = torch.arange(L - n, L, device=DEV)[:, None]
+        j = torch.arange(L, device=DEV)[None]
+        hidden = j > p
+        if c["window"]:
+            hidden = hidden | ((p - j >= c["window"]) & (j >= c["sinks"]))
+        for h in range(Hkv):
+            k, v = _values64(s, "k", b, h, L), _values64(s, "v", b, h, L)
+            for hq in range(h * (Hq // Hkv), (h + 1) * (Hq // Hkv)):
+                z = (s["q"][hq, cu[b]:cu[b + 1]].double() @ k.T) * s["scale"]
+                z[hidden] = -math.inf
+                lse[hq, cu[b]:cu[b + 1]] = torch.logsumexp(z, -1)
+                out[cu[b]:cu[b + 1], hq] = torch.softmax(z, -1) @ v
+    r = {"out": out.reshape(s["M"], Hq * D)}
+    if c["lse"]:
+        r["lse"] = lse
+    return r
