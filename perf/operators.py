@@ -270,7 +270,7 @@ def run(state):
                                interleaved=c["interleaved"])["q"]
         if c["fmt"] == "bf16":
             return {"q": q, "k_pages": s["k_pages"], "v_pages": s["v_pages"]}
-        back = fnl.kv_gather(h, s["cache"], s["batch"])
+        back = fnl.kv_gather(h, s["cache"], s["batch"], M=s["M"])
         return {"q": q, "k": back["k"], "v": back["v"]}
     lse = torch.empty(c["Hq"], s["M"], dtype=torch.float32, device=DEV) if c["lse"] else None
     r = fnl.paged_attention(h, s["cache"], s["batch"], s["q"], scale=s["scale"], window=c["window"],
