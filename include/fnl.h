@@ -85,7 +85,7 @@ typedef enum {
   FNL_ERR_ALIAS = 3,          /* an output overlaps an input or another output */
   FNL_ERR_UNSUPPORTED = 4,    /* shape outside what the kernels handle (K > 32768, ...) */
   FNL_ERR_CUDA = 5,           /* CUDA runtime/driver error (allocation, launch) */
-  FNL_ERR_DEVICE_STATUS = 6   /* a kernel's bounded wait gave up (see fnl_check) */
+  FNL_ERR_DEVICE_STATUS = 6   /* a kernel's bounded wait gave up, or a paged batch did not fit (see fnl_check) */
 } fnl_status;
 
 typedef enum { FNL_NORM_LAYERNORM = 0, FNL_NORM_RMSNORM = 1 } fnl_norm;
@@ -163,7 +163,8 @@ const char* fnl_last_plan(const fnl_handle* h);
  * FNL_ERR_DEVICE_STATUS if a kernel since the last check gave up a wait
  * (device codes 1-7) or, in the debug build libfnl_debug.so (compiled with
  * FNL_DEBUG_CHECKS), skipped an output store that would have left its buffer
- * (device code 8); fnl_last_error() names the code. The outputs of the calls
+ * (device code 8), or a paged-cache call met a batch description that does not
+ * fit its cache (device code 9, see fnl_kv_batch); fnl_last_error() names the code. The outputs of the calls
  * since the last check are then not to be trusted. It
  * also resets the handle's split-K arrival counters (an aborted CTA leaves its
  * tiles' counters part-way), so later calls on the handle compute correctly. */
@@ -297,6 +298,110 @@ fnl_status fnl_quantize_weight_fp8(fnl_handle* h, fnl_stream stream, const fnl_b
 fnl_status fnl_linear_add_residual(fnl_handle* h, fnl_stream stream, const fnl_bf16* a, const fnl_bf16* W,
                                    const fnl_bf16* bias, const fnl_bf16* residual, fnl_bf16* out, int M, int K,
                                    int N);
+
+/* ---------------------------------------------------------------------------
+ * The paged key/value cache, between the QKV projection (q [Hq, M, D], k and v
+ * [Hkv, M, D], as fnl_add_norm_qkv writes them) and the output projection
+ * (fnl_linear_add_residual, whose operand is the attention's out [M, Hq * D]).
+ * Paged KV blocks: TensorRT-LLM 深度工程实践, §3.2 (a block holds a fixed number
+ * of tokens, 128 on the page); the prefill / decode split of a batch into two
+ * calls is the page's micro-batches (§3.1).
+ *
+ * A cache holds num_pages pages of page_size tokens (a power of two, 16..1024)
+ * for Hkv heads of D (64 or 128) values. Per page: head h, token t, value d.
+ *   FNL_KV_BF16  k, v  bf16 [num_pages, Hkv, page_size, D]; k_scale = v_scale = NULL
+ *   FNL_KV_INT4  k, v  uint8 [num_pages, Hkv, page_size, D / 2], value d in byte
+ *                d / 2, the even d in the low nibble;
+ *                k_scale, v_scale  bf16 [num_pages, Hkv, page_size, 2]: the row's
+ *                scale s and minimum lo. A code c in 0..15 stands for lo + c s.
+ * A row is coded by lo = min x, s = (max x - lo) / 15 rounded up to bf16,
+ * c = round((x - lo) / s) (to nearest even, in fp32; 0 where s = 0): every value
+ * is within s / 2 of what its code stands for. Rows have to be finite.
+ * Pages may lie apart: page_stride bytes from page to page in k and in v (0:
+ * dense; a multiple of 16), scale_page_stride in the scales (0: dense), so that k
+ * and v may be the halves of one [num_pages, 2, ...] allocation. */
+typedef enum { FNL_KV_BF16 = 0, FNL_KV_INT4 = 1 } fnl_kv_format;
+
+typedef struct {
+  int format;                    /* fnl_kv_format */
+  int num_pages, page_size;
+  int Hkv, D;
+  void* k;
+  void* v;
+  fnl_bf16* k_scale;
+  fnl_bf16* v_scale;
+  long long page_stride;
+  long long scale_page_stride;
+} fnl_kv_cache;
+
+/* A batch of B sequences, packed: sequence b's new tokens are rows cu_q[b] ..
+ * cu_q[b + 1] - 1 of the M rows of q, k, v and out; kv_len[b] is its length in
+ * the cache, the new tokens included; so new token i of n has the position
+ * kv_len[b] - n + i. Position t is row t % page_size of page
+ * block_table[b * max_pages + t / page_size]. cu_q, kv_len and block_table are
+ * DEVICE arrays that the kernels read when they run (a captured graph replays
+ * with their new contents); max_q is the caller's bound on any sequence's new
+ * tokens. Sequences without new tokens, and rows behind cu_q[B], are allowed: such
+ * rows of the outputs are left as they were. Entries of block_table that no
+ * visible position needs are not read (pages that have left a window may be
+ * reused).
+ * The arrays' contents cannot be checked on the host: a page id outside
+ * [0, num_pages), a position outside the block table or the rotation table, a
+ * sequence longer than max_q or with kv_len[b] < n is met without touching memory
+ * outside the buffers and recorded as device code 9, which fnl_check reports as
+ * FNL_ERR_DEVICE_STATUS; the outputs of that call are then not to be trusted. Two
+ * sequences of a batch may share pages that neither of them appends to. */
+typedef struct {
+  int B;
+  int max_q;
+  const int* cu_q;               /* [B + 1], ascending from 0 */
+  const int* kv_len;             /* [B] */
+  const int* block_table;        /* [B, max_pages] */
+  int max_pages;
+} fnl_kv_batch;
+
+/* Rotation by position, and the append of the batch's keys and values.
+ * The first rot_dim (a multiple of 16, at most D) values of every head of q and k
+ * are rotated by their token's angles: for pair i, (a, b) -> (a c - b s, b c + a s)
+ * with c = cos[pos, i], s = sin[pos, i], pair i being values (i, i + rot_dim / 2),
+ * or (2i, 2i + 1) when interleaved = 1. cos and sin are fp32 [max_pos, rot_dim / 2]
+ * tables of the caller (any base or scaling of the frequencies). Products and sums
+ * are rounded to fp32 one by one and the result to bf16. q_out [Hq, M, D] gets the
+ * rotated q and may be q itself; k (rotated) and v [Hkv, M, D] go to their pages,
+ * coded when the cache is FNL_KV_INT4 (k from its rotated bf16 values).
+ * rot_dim = 0: no rotation; q, q_out, cos and sin must then be NULL. One kernel.
+ * Errors: FNL_ERR_INVALID_ARG, FNL_ERR_ALIGNMENT (16 bytes for tensors, 4 for
+ * integer lists and scales), FNL_ERR_ALIAS (q_out partly on q, or a tensor on the
+ * cache), FNL_ERR_UNSUPPORTED (D, page_size, B > 65535). */
+fnl_status fnl_rope_append_kv(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch,
+                              int M, int Hq, const fnl_bf16* q, const fnl_bf16* k, const fnl_bf16* v,
+                              const float* cos, const float* sin, int rot_dim, int max_pos, int interleaved,
+                              fnl_bf16* q_out);
+
+/* The batch's new tokens read back from their pages: k_out, v_out bf16
+ * [Hkv, M, D], for 4-bit pages the values that the codes stand for, rounded to
+ * bf16. With cu_q covering whole sequences it unpacks them (to hand a prefix to
+ * other code, to move it to another cache). One kernel. */
+fnl_status fnl_kv_gather(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch, int M,
+                         fnl_bf16* k_out, fnl_bf16* v_out);
+
+/* Causal attention of the batch's new tokens over the cache (their own keys and
+ * values, already appended, included):
+ *   out[m, hq * D + d] = sum_j p_j v[j, d],  p = softmax_j(scale q[hq, m] . k[j])
+ * over the positions j <= pos(m) of head hq / (Hq / Hkv); with window > 0 only
+ * those with j > pos(m) - window or j < sinks (first tokens that stay visible;
+ * sinks need a window). A token that sees nothing gets 0. lse (nullable, fp32
+ * [Hq, M]): log sum_j exp(scale q . k[j]), -inf where nothing is seen, for joining
+ * with the attention over another cache. Scores, softmax and sums are fp32; the
+ * probabilities are rounded to bf16 for the product with v; 4-bit keys and values
+ * are used unrounded. Slots of the cache that no token of the batch sees are not
+ * read, whatever they hold; visible ones have to be finite.
+ * Any mix of lengths is correct; a batch of few new tokens per sequence (at most
+ * 16 rows max_q * Hq / Hkv) runs the form that splits the keys over the whole GPU,
+ * so decode steps and prompts are best given as two calls. */
+fnl_status fnl_paged_attention(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch,
+                               int M, int Hq, const fnl_bf16* q, float scale, int window, int sinks, fnl_bf16* out,
+                               float* lse);
 
 /* Allocation-free variant of fnl_add_norm_qkv for decode-sized batches.
  * The pages have no counterpart to this entry point. It is for callers that

@@ -103,3 +103,4 @@ from .core import (  # noqa: F401
     add_bias_norm_gelu_fp8,
     run,
 )
+from . import paged  # noqa: F401,E402

@@ -12,6 +12,11 @@ from .fnl import (  # noqa: F401
     add_norm_qkv,
     add_norm_qkv_static,
     add_norm_swiglu,
+    KVBatch,
+    KVCache,
+    kv_gather,
+    paged_attention,
+    rope_append_kv,
     lib,
     lib_path,
     run_workload,

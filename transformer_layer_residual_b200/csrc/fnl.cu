@@ -25,6 +25,8 @@
 #include "k3_splitk.cuh"
 #include "k4_pair.cuh"
 #include "k5_tp.cuh"
+#include "k7_kv.cuh"
+#include "k8_attend.cuh"
 
 using fnl::bf16;
 using fnl::OpParams;
@@ -100,6 +102,9 @@ struct fnl_handle {
   std::string plan_text;     // the last call's plan (fnl_last_plan)
   int pairs = 0;             // resident CTA pairs of the pair kernel (0: not queried yet)
   std::vector<fnlh::TunedEntry> tuned;   // shape auto-tuning cache
+  // Paged-cache calls: [status][arrival counters][partial sums], one fixed block
+  // that never moves (a captured graph keeps its addresses).
+  uint8_t* kv_ws = nullptr;
 };
 
 namespace {
@@ -120,6 +125,15 @@ int qkv_columns(int Hq, int Hkv, int D) {
   if (Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
   const long long n = (static_cast<long long>(Hq) + 2LL * Hkv) * D;
   return n <= kMaxN ? static_cast<int>(n) : 0;
+}
+
+// Paged-cache block: status word, one arrival counter and two partial-sum slots
+// per block of the attention kernel's split form (two blocks an SM at most).
+constexpr int kKvBlocksPerSm = 2;
+size_t kv_fixed_bytes(const fnl_handle* h) { return kStatusBytes + static_cast<size_t>(h->num_sms) * kKvBlocksPerSm * 4; }
+size_t kv_part_offset(const fnl_handle* h) { return (kv_fixed_bytes(h) + 255) & ~static_cast<size_t>(255); }
+size_t kv_ws_bytes(const fnl_handle* h) {
+  return kv_part_offset(h) + static_cast<size_t>(h->num_sms) * kKvBlocksPerSm * 2 * fnl::k8::kPartFloats * 4;
 }
 
 size_t align256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
@@ -1129,7 +1143,12 @@ fnl_status fnl_create(fnl_handle** out, int device, const fnl_options* opt) {
     need += align256(T * seg * fnl::k3::MAX_MPAD * 4) + align256(T * seg * fnl::k3::MAX_MPAD * 128 * 4);
   }
   fnl_status st = ensure_workspace(h, nullptr, need);
+  if (st == FNL_OK && (cudaMalloc(&h->kv_ws, kv_ws_bytes(h)) != cudaSuccess ||
+                       cudaMemset(h->kv_ws, 0, kv_ws_bytes(h)) != cudaSuccess))
+    st = FNL_ERR_CUDA;
   if (st != FNL_OK) {
+    if (h->ws) cudaFree(h->ws);
+    if (h->kv_ws) cudaFree(h->kv_ws);
     delete h;
     return st;
   }
@@ -1142,6 +1161,7 @@ fnl_status fnl_destroy(fnl_handle* h) {
   cudaSetDevice(h->device);
   cudaDeviceSynchronize();
   if (h->ws) cudaFree(h->ws);
+  if (h->kv_ws) cudaFree(h->kv_ws);
   delete h;
   return FNL_OK;
 }
@@ -1168,19 +1188,23 @@ fnl_status fnl_check(fnl_handle* h, fnl_stream stream) {
   cudaSetDevice(h->device);
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(h, e, "cudaStreamSynchronize");
-  int status = 0;
+  int status = 0, kv_status = 0;
   e = cudaMemcpy(&status, h->ws, sizeof(int), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(h, e, "cudaMemcpy(status)");
-  if (status != 0) {
+  e = cudaMemcpy(&kv_status, h->kv_ws, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return cuda_fail(h, e, "cudaMemcpy(status of the paged-cache calls)");
+  if (status != 0 || kv_status != 0) {
     // A CTA that gave up never made its split-K arrival, so its tiles' arrival
     // counters are left part-way; clear them with the status word, or every later
     // call would elect the wrong last CTA.
     e = cudaMemset(h->ws, 0, kFixedBytes);
+    if (e == cudaSuccess) e = cudaMemset(h->kv_ws, 0, kv_fixed_bytes(h));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(h, e, "cudaMemset(status, counters)");
     return fail(h, FNL_ERR_DEVICE_STATUS,
                 "device status %d (1-7: a kernel gave up a bounded wait; 8: a debug build refused an out-of-range "
-                "store)", status);
+                "store; 9: a paged-cache call met a batch description outside its cache)",
+                status != 0 ? status : kv_status);
   }
   return FNL_OK;
 }
@@ -1347,6 +1371,257 @@ fnl_status fnl_linear_add_residual(fnl_handle* h, fnl_stream stream, const fnl_b
   c.norm = FNL_NORM_RMSNORM; c.eps = 1.f;   // unused (no norm)
   c.M = M; c.K = K; c.N = N;
   return run(h, c);
+}
+
+}  // extern "C"
+
+// ============================================================================
+// The paged key/value cache: append with rotation, read-back, attention.
+// ============================================================================
+namespace {
+
+using fnl::KvParams;
+
+// Checks the cache and the batch and fills the kernels' parameters. `what` names
+// the outputs for messages only.
+fnl_status kv_params(fnl_handle* h, const fnl_kv_cache* c, const fnl_kv_batch* b, int M, KvParams* p) {
+  if (!h) return FNL_ERR_INVALID_ARG;
+  if (!c || !b) return fail(h, FNL_ERR_INVALID_ARG, "cache and batch are required");
+  if (c->format != FNL_KV_BF16 && c->format != FNL_KV_INT4)
+    return fail(h, FNL_ERR_INVALID_ARG, "format must be FNL_KV_BF16 or FNL_KV_INT4");
+  const bool int4 = c->format == FNL_KV_INT4;
+  if (M < 0 || b->B < 0 || b->max_q < 0 || b->max_pages < 0 || c->num_pages < 0)
+    return fail(h, FNL_ERR_INVALID_ARG, "need M, B, max_q, max_pages and num_pages >= 0");
+  if (c->Hkv <= 0 || c->Hkv > 65535) return fail(h, FNL_ERR_INVALID_ARG, "need 1 <= Hkv <= 65535 (Hkv=%d)", c->Hkv);
+  if (c->D != 64 && c->D != 128) return fail(h, FNL_ERR_UNSUPPORTED, "D must be 64 or 128 (D=%d)", c->D);
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+    return fail(h, FNL_ERR_UNSUPPORTED, "page_size must be a power of two in [16, 1024] (page_size=%d)", c->page_size);
+  if (b->B > 65535) return fail(h, FNL_ERR_UNSUPPORTED, "B=%d exceeds 65535", b->B);
+  if (static_cast<long long>(b->max_pages) * c->page_size > 0x7fffff00LL)
+    return fail(h, FNL_ERR_UNSUPPORTED, "max_pages * page_size must stay below 2^31 - 256 positions");
+  const long long row_bytes = int4 ? c->D / 2 : 2 * c->D;
+  const long long page_rows = static_cast<long long>(c->Hkv) * c->page_size;
+  const long long stride = c->page_stride ? c->page_stride : page_rows * row_bytes;
+  const long long sstride = c->scale_page_stride ? c->scale_page_stride : page_rows * 4;
+  if (page_rows > 0x7fffffffLL) return fail(h, FNL_ERR_UNSUPPORTED, "Hkv * page_size must stay below 2^31");
+  if (stride < page_rows * row_bytes || (int4 && sstride < page_rows * 4))
+    return fail(h, FNL_ERR_INVALID_ARG, "a page stride is smaller than a page");
+  if (stride % 16 || (int4 && sstride % 4))
+    return fail(h, FNL_ERR_ALIGNMENT, "page_stride must be a multiple of 16 bytes, scale_page_stride of 4");
+  p->k = static_cast<uint8_t*>(c->k);
+  p->v = static_cast<uint8_t*>(c->v);
+  p->k_scale = reinterpret_cast<uint32_t*>(c->k_scale);
+  p->v_scale = reinterpret_cast<uint32_t*>(c->v_scale);
+  p->page_stride = stride;
+  p->scale_stride = sstride / 4;
+  p->num_pages = c->num_pages;
+  p->page_shift = 0;
+  while ((1 << p->page_shift) < c->page_size) ++p->page_shift;
+  p->Hkv = c->Hkv;
+  p->B = b->B;
+  p->M = M;
+  p->max_q = b->max_q;
+  p->max_pages = b->max_pages;
+  p->cu_q = b->cu_q;
+  p->kv_len = b->kv_len;
+  p->table = b->block_table;
+  if (M == 0 || b->B == 0) return FNL_OK;
+  if (!c->k || !c->v || (int4 && (!c->k_scale || !c->v_scale)))
+    return fail(h, FNL_ERR_INVALID_ARG, "k and v (and k_scale and v_scale of 4-bit pages) are required");
+  if (!int4 && (c->k_scale || c->v_scale))
+    return fail(h, FNL_ERR_INVALID_ARG, "k_scale and v_scale must be NULL for bf16 pages");
+  if (!b->cu_q || !b->kv_len || !b->block_table)
+    return fail(h, FNL_ERR_INVALID_ARG, "cu_q, kv_len and block_table are required");
+  if (!al16(c->k) || !al16(c->v)) return fail(h, FNL_ERR_ALIGNMENT, "k and v must be 16-byte aligned");
+  const void* p4[] = {c->k_scale, c->v_scale, b->cu_q, b->kv_len, b->block_table};
+  for (const void* q : p4)
+    if (q && !al4(q)) return fail(h, FNL_ERR_ALIGNMENT, "scales, cu_q, kv_len and block_table must be 4-byte aligned");
+  p->status = reinterpret_cast<int*>(h->kv_ws);
+  cudaError_t e = cudaSetDevice(h->device);
+  if (e != cudaSuccess) return cuda_fail(h, e, "cudaSetDevice");
+  return FNL_OK;
+}
+
+// The caller's regions that a paged-cache call reads or writes. Pages may be
+// interleaved (k and v in one allocation), so a cache counts as its spans.
+size_t cache_span(const fnl_kv_cache* c, const KvParams& p, bool scales) {
+  if (c->num_pages <= 0) return 0;
+  const long long rows = static_cast<long long>(c->Hkv) * c->page_size;
+  const long long last = rows * (scales ? 4 : (c->format == FNL_KV_INT4 ? c->D / 2 : 2 * c->D));
+  return static_cast<size_t>((c->num_pages - 1) * (scales ? p.scale_stride * 4 : p.page_stride) + last);
+}
+fnl_status cache_alias(fnl_handle* h, const fnl_kv_cache* c, const fnl_kv_batch* b, const KvParams& p, const Range* io,
+                       int n) {
+  const bool int4 = c->format == FNL_KV_INT4;
+  const Range mem[] = {{c->k, cache_span(c, p, false), "k pages"},
+                       {c->v, cache_span(c, p, false), "v pages"},
+                       {int4 ? c->k_scale : nullptr, cache_span(c, p, true), "k scales"},
+                       {int4 ? c->v_scale : nullptr, cache_span(c, p, true), "v scales"}};
+  const Range lists[] = {{b->cu_q, (static_cast<size_t>(b->B) + 1) * 4, "cu_q"},
+                         {b->kv_len, static_cast<size_t>(b->B) * 4, "kv_len"},
+                         {b->block_table, static_cast<size_t>(b->B) * b->max_pages * 4, "block_table"}};
+  for (int i = 0; i < n; ++i) {
+    for (const Range& m : mem)
+      if (overlap(io[i], m)) return fail(h, FNL_ERR_ALIAS, "%s overlaps the cache's %s", io[i].name, m.name);
+    for (const Range& m : lists)
+      if (overlap(io[i], m)) return fail(h, FNL_ERR_ALIAS, "%s overlaps %s", io[i].name, m.name);
+  }
+  return FNL_OK;
+}
+
+template <typename Kern, typename Params>
+fnl_status kv_launch(fnl_handle* h, Kern kern, dim3 grid, int threads, int smem, cudaStream_t stream, const Params& p) {
+  fnl_status st = FNL_OK;
+  if (smem > 48 * 1024 && (st = set_smem(h, kern, smem)) != FNL_OK) return st;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];   // every kernel here waits for its predecessor before it touches memory
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess) return cuda_fail(h, e, "launch of a paged-cache kernel");
+  return FNL_OK;
+}
+
+// Tokens per block: the most (a power of two, at most 8) that still leaves two
+// blocks for every SM, so that the angles of a token serve as many heads as
+// possible without idle SMs.
+int kv_tokens(const fnl_handle* h, int M) {
+  int t = 1;
+  while (t < 8 && M / (2 * t) >= 2 * h->num_sms) t *= 2;
+  return t;
+}
+
+template <int D, int FMT>
+fnl_status append_launch(fnl_handle* h, bool interleaved, dim3 grid, cudaStream_t s, const fnl::AppendParams& p) {
+  if (interleaved) return kv_launch(h, fnl::k7_append<D, FMT, true>, grid, fnl::kKvThreads, 0, s, p);
+  return kv_launch(h, fnl::k7_append<D, FMT, false>, grid, fnl::kKvThreads, 0, s, p);
+}
+
+template <int D, int FMT>
+fnl_status attend_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p) {
+  char buf[160];
+  if (static_cast<long long>(p.kv.max_q) * p.group <= fnl::k8::kRowsMax) {
+    typedef fnl::k8::SplitCfg<D, FMT> C;
+    static_assert(C::BLOCKS <= kKvBlocksPerSm, "workspace slots per SM");
+    const int grid = h->num_sms * C::BLOCKS;
+    snprintf(buf, sizeof(buf), "paged attention, split form, grid %d", grid);
+    h->plan_text = buf;
+    return kv_launch(h, fnl::k8::k8_attend_split<D, FMT>, dim3(grid), C::THREADS, C::SMEM, s, p);
+  }
+  typedef fnl::k8::RowsCfg<D, FMT> C;
+  const long long tiles = (static_cast<long long>(p.kv.max_q) * p.group + C::ROWS - 1) / C::ROWS;
+  if (tiles > 0x7fffffffLL) return fail(h, FNL_ERR_UNSUPPORTED, "max_q * Hq / Hkv is too large");
+  snprintf(buf, sizeof(buf), "paged attention, row form, grid %lld x %d x %d", tiles, p.kv.Hkv, p.kv.B);
+  h->plan_text = buf;
+  return kv_launch(h, fnl::k8::k8_attend_rows<D, FMT>, dim3(static_cast<unsigned>(tiles), p.kv.Hkv, p.kv.B), C::THREADS,
+                   C::SMEM, s, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+fnl_status fnl_rope_append_kv(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch,
+                              int M, int Hq, const fnl_bf16* q, const fnl_bf16* k, const fnl_bf16* v, const float* cos,
+                              const float* sin, int rot_dim, int max_pos, int interleaved, fnl_bf16* q_out) {
+  fnl::AppendParams p{};
+  fnl_status st = kv_params(h, cache, batch, M, &p.kv);
+  if (st != FNL_OK) return st;
+  if (rot_dim < 0 || rot_dim % 16 || rot_dim > cache->D)
+    return fail(h, FNL_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [0, D] (rot_dim=%d)", rot_dim);
+  if (rot_dim > 0 && (Hq <= 0 || Hq % cache->Hkv))
+    return fail(h, FNL_ERR_INVALID_ARG, "Hq (%d) must be a positive multiple of Hkv (%d)", Hq, cache->Hkv);
+  if (Hq < 0 || Hq > (1 << 20)) return fail(h, FNL_ERR_INVALID_ARG, "need 0 <= Hq <= 2^20 (Hq=%d)", Hq);
+  if (interleaved != 0 && interleaved != 1) return fail(h, FNL_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if (M == 0 || batch->B == 0) return FNL_OK;
+  if (!k || !v) return fail(h, FNL_ERR_INVALID_ARG, "k and v are required");
+  if (rot_dim > 0 && (!q || !q_out || !cos || !sin || max_pos <= 0))
+    return fail(h, FNL_ERR_INVALID_ARG, "a rotation needs q, q_out, cos, sin and max_pos > 0");
+  if (rot_dim == 0 && (q || q_out || cos || sin))
+    return fail(h, FNL_ERR_INVALID_ARG, "q, q_out, cos and sin must be NULL without a rotation (rot_dim = 0)");
+  const void* p16[] = {q, k, v, q_out, cos, sin};
+  for (const void* x : p16)
+    if (x && !al16(x)) return fail(h, FNL_ERR_ALIGNMENT, "q, k, v, q_out, cos and sin must be 16-byte aligned");
+  const size_t tq = static_cast<size_t>(Hq) * M * cache->D * 2, tk = static_cast<size_t>(cache->Hkv) * M * cache->D * 2;
+  const size_t tab = static_cast<size_t>(std::max(max_pos, 0)) * rot_dim * 2;
+  const Range io[] = {{q_out, tq, "q_out"}, {q, tq, "q"}, {k, tk, "k"}, {v, tk, "v"}, {cos, tab, "cos"}, {sin, tab, "sin"}};
+  if ((st = cache_alias(h, cache, batch, p.kv, io, 6)) != FNL_OK) return st;
+  for (int i = 1; i < 6; ++i)
+    if (!(i == 1 && q_out == q) && overlap(io[0], io[i]))
+      return fail(h, FNL_ERR_ALIAS, "q_out overlaps %s%s", io[i].name, i == 1 ? " without being the same buffer" : "");
+  p.q = B(q); p.k = B(k); p.v = B(v); p.q_out = Bm(q_out);
+  p.cos = cos; p.sin = sin; p.Hq = Hq; p.rot = rot_dim; p.max_pos = max_pos;
+  p.tokens = kv_tokens(h, M);
+  const dim3 grid((M + p.tokens - 1) / p.tokens);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool il = interleaved != 0, int4 = cache->format == FNL_KV_INT4;
+  if (cache->D == 64)
+    return int4 ? append_launch<64, fnl::kKvInt4>(h, il, grid, s, p) : append_launch<64, fnl::kKvBf16>(h, il, grid, s, p);
+  return int4 ? append_launch<128, fnl::kKvInt4>(h, il, grid, s, p) : append_launch<128, fnl::kKvBf16>(h, il, grid, s, p);
+}
+
+fnl_status fnl_kv_gather(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch, int M,
+                         fnl_bf16* k_out, fnl_bf16* v_out) {
+  fnl::GatherParams p{};
+  fnl_status st = kv_params(h, cache, batch, M, &p.kv);
+  if (st != FNL_OK || M == 0 || batch->B == 0) return st;
+  if (!k_out || !v_out) return fail(h, FNL_ERR_INVALID_ARG, "k_out and v_out are required");
+  if (!al16(k_out) || !al16(v_out)) return fail(h, FNL_ERR_ALIGNMENT, "k_out and v_out must be 16-byte aligned");
+  const size_t tk = static_cast<size_t>(cache->Hkv) * M * cache->D * 2;
+  const Range io[] = {{k_out, tk, "k_out"}, {v_out, tk, "v_out"}};
+  if ((st = cache_alias(h, cache, batch, p.kv, io, 2)) != FNL_OK) return st;
+  if (overlap(io[0], io[1])) return fail(h, FNL_ERR_ALIAS, "k_out and v_out overlap");
+  p.k_out = Bm(k_out); p.v_out = Bm(v_out);
+  p.tokens = kv_tokens(h, M);
+  const dim3 grid((M + p.tokens - 1) / p.tokens);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool int4 = cache->format == FNL_KV_INT4;
+  if (cache->D == 64)
+    return int4 ? kv_launch(h, fnl::k7_gather<64, fnl::kKvInt4>, grid, fnl::kKvThreads, 0, s, p)
+                : kv_launch(h, fnl::k7_gather<64, fnl::kKvBf16>, grid, fnl::kKvThreads, 0, s, p);
+  return int4 ? kv_launch(h, fnl::k7_gather<128, fnl::kKvInt4>, grid, fnl::kKvThreads, 0, s, p)
+              : kv_launch(h, fnl::k7_gather<128, fnl::kKvBf16>, grid, fnl::kKvThreads, 0, s, p);
+}
+
+fnl_status fnl_paged_attention(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch,
+                               int M, int Hq, const fnl_bf16* q, float scale, int window, int sinks, fnl_bf16* out,
+                               float* lse) {
+  fnl::AttnParams p{};
+  fnl_status st = kv_params(h, cache, batch, M, &p.kv);
+  if (st != FNL_OK) return st;
+  if (Hq <= 0 || Hq > (1 << 20) || Hq % cache->Hkv)
+    return fail(h, FNL_ERR_INVALID_ARG, "Hq (%d) must be a positive multiple of Hkv (%d), at most 2^20", Hq, cache->Hkv);
+  if (!(scale > 0.f) || scale > 1e30f) return fail(h, FNL_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
+    return fail(h, FNL_ERR_INVALID_ARG, "window and sinks must be >= 0, and sinks need a window");
+  if (static_cast<long long>(batch->max_q) * (Hq / cache->Hkv) > 0x7fffff00LL)
+    return fail(h, FNL_ERR_UNSUPPORTED, "max_q * Hq / Hkv must stay below 2^31 - 256 rows");
+  if (M == 0 || batch->B == 0) return FNL_OK;
+  if (batch->max_q == 0) return fail(h, FNL_ERR_INVALID_ARG, "max_q must be > 0 for a batch with tokens");
+  if (!q || !out) return fail(h, FNL_ERR_INVALID_ARG, "q and out are required");
+  if (!al16(q) || !al16(out)) return fail(h, FNL_ERR_ALIGNMENT, "q and out must be 16-byte aligned");
+  if (lse && !al4(lse)) return fail(h, FNL_ERR_ALIGNMENT, "lse must be 4-byte aligned");
+  const size_t tq = static_cast<size_t>(Hq) * M * cache->D * 2;
+  const Range io[] = {{out, tq, "out"}, {lse, static_cast<size_t>(Hq) * M * 4, "lse"}, {q, tq, "q"}};
+  if ((st = cache_alias(h, cache, batch, p.kv, io, 2)) != FNL_OK) return st;
+  if (overlap(io[0], io[2]) || overlap(io[1], io[2]) || overlap(io[0], io[1]))
+    return fail(h, FNL_ERR_ALIAS, "q, out and lse must not overlap");
+  p.q = B(q); p.out = Bm(out); p.lse = lse;
+  p.Hq = Hq; p.group = Hq / cache->Hkv;
+  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.window = window; p.sinks = sinks;
+  p.counters = reinterpret_cast<unsigned*>(h->kv_ws + kStatusBytes);
+  p.part = reinterpret_cast<float*>(h->kv_ws + kv_part_offset(h));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool int4 = cache->format == FNL_KV_INT4;
+  if (cache->D == 64) return int4 ? attend_launch<64, fnl::kKvInt4>(h, s, p) : attend_launch<64, fnl::kKvBf16>(h, s, p);
+  return int4 ? attend_launch<128, fnl::kKvInt4>(h, s, p) : attend_launch<128, fnl::kKvBf16>(h, s, p);
 }
 
 }  // extern "C"

@@ -25,12 +25,14 @@ STATUS_NAMES = {0: "FNL_OK", 1: "FNL_ERR_INVALID_ARG", 2: "FNL_ERR_ALIGNMENT", 3
 NORMS = {"layernorm": 0, "rmsnorm": 1}
 PATHS = {"auto": 0, "tile": 1, "splitk": 2, "wide": 3, "cluster": 4, "pair": 5, "pair_sk": 6}
 PRECISIONS = {"default": 0, "split": 1, "single": 2}
+KV_FORMATS = {"bf16": 0, "int4": 1}
 
 EXPORTED = ("fnl_create", "fnl_destroy", "fnl_status_string", "fnl_last_error", "fnl_last_plan", "fnl_check",
             "fnl_add_norm_qkv", "fnl_add_norm_swiglu", "fnl_add_bias_norm_gelu", "fnl_linear_add_residual",
             "fnl_add_norm_qkv_fp8", "fnl_add_norm_swiglu_fp8", "fnl_add_bias_norm_gelu_fp8",
             "fnl_quantize_weight_fp8", "fnl_tp_allreduce",
-            "fnl_add_norm_qkv_static", "fnl_check_static")
+            "fnl_add_norm_qkv_static", "fnl_check_static",
+            "fnl_rope_append_kv", "fnl_kv_gather", "fnl_paged_attention")
 
 
 class FnlError(RuntimeError):
@@ -43,6 +45,18 @@ class _Options(ctypes.Structure):
     _fields_ = [("max_tokens", ctypes.c_int), ("max_n", ctypes.c_int), ("path", ctypes.c_int),
                 ("max_ctas", ctypes.c_int), ("precision", ctypes.c_int), ("wait_ns", ctypes.c_longlong),
                 ("debug_stall_calls", ctypes.c_int), ("tune", ctypes.c_int)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_longlong),
+                ("scale_page_stride", ctypes.c_longlong)]
+
+
+class _KvBatch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("max_q", ctypes.c_int), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("max_pages", ctypes.c_int)]
 
 
 def lib_path() -> str:
@@ -79,6 +93,10 @@ def lib() -> ctypes.CDLL:
     L.fnl_add_bias_norm_gelu_fp8.argtypes = [P, P, P, P, P, P, P, P, I, F, P, P, P, I, I, I, P, P, P]
     L.fnl_add_norm_qkv_static.argtypes = [P, P, P, P, P, P, I, F, P, P, I, I, I, I, I, P, P, P, P, P]
     L.fnl_check_static.argtypes = [P]
+    KC, KB = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch)
+    L.fnl_rope_append_kv.argtypes = [P, P, KC, KB, I, I, P, P, P, P, P, I, I, I, P]
+    L.fnl_kv_gather.argtypes = [P, P, KC, KB, I, P, P]
+    L.fnl_paged_attention.argtypes = [P, P, KC, KB, I, I, P, F, I, I, P, P]
     for name in EXPORTED:
         if getattr(L, name).restype is None and name not in ("fnl_status_string", "fnl_last_error", "fnl_last_plan"):
             getattr(L, name).restype = I
@@ -392,6 +410,172 @@ def add_bias_norm_gelu_fp8(h: Handle, x, residual, gamma, beta, Wq, w_scale, bia
     if st != FNL_OK:
         h._raise(st, "fnl_add_bias_norm_gelu_fp8")
     return {"residual_out": residual_out, "out": out, "mean": mean_out, "rstd": rstd_out}
+
+
+class KVCache:
+    """A paged key/value cache (fnl_kv_cache) over the caller's tensors.
+
+    bf16: k, v [num_pages, Hkv, page_size, D] bfloat16. int4: k, v uint8
+    [num_pages, Hkv, page_size, D / 2] (the even d in the low nibble) with k_scale,
+    v_scale bfloat16 [num_pages, Hkv, page_size, 2] (scale, minimum). The page
+    dimension may be strided (k and v as halves of one allocation); the others are
+    contiguous. The object holds the tensors; it may be kept for the cache's life."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dtype not in (torch.bfloat16, torch.uint8):
+            raise ValueError(f"k must be torch.bfloat16 or torch.uint8, got {k.dtype}")
+        self.format = "bf16" if k.dtype == torch.bfloat16 else "int4"
+        if k.dim() != 4:
+            raise ValueError("k must be [num_pages, Hkv, page_size, D] (D / 2 bytes for int4)")
+        n, self.Hkv, self.page_size, last = k.shape
+        self.D = last if self.format == "bf16" else 2 * last
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        stride = self._pages(k, "k", k.shape, k.dtype)
+        if self._pages(v, "v", k.shape, k.dtype) != stride:
+            raise ValueError("k and v must have the same page stride")
+        scale_stride = 0
+        if self.format == "int4":
+            shape = (n, self.Hkv, self.page_size, 2)
+            scale_stride = self._pages(k_scale, "k_scale", shape, torch.bfloat16)
+            if self._pages(v_scale, "v_scale", shape, torch.bfloat16) != scale_stride:
+                raise ValueError("k_scale and v_scale must have the same page stride")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no k_scale and v_scale")
+        self.device = k.device
+        self.c = _KvCache(KV_FORMATS[self.format], n, self.page_size, self.Hkv, self.D, _p(k), _p(v), _p(k_scale),
+                          _p(v_scale), stride, scale_stride)
+
+    @staticmethod
+    def _pages(t, name, shape, dtype):
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        inner = (shape[2] * shape[3], shape[3], 1)
+        if any(st != want for st, want, n in zip(t.stride()[1:], inner, shape[1:]) if n > 1):
+            raise ValueError(f"{name} must be contiguous within a page")
+        return t.stride(0) * t.element_size() if shape[0] > 1 else 0
+
+    @classmethod
+    def empty(cls, num_pages, page_size, Hkv, D, format="bf16", device="cuda"):
+        """A new, uninitialised cache."""
+        if format not in KV_FORMATS:
+            raise ValueError(f"format must be one of {list(KV_FORMATS)}")
+        if format == "bf16":
+            return cls(*(torch.empty(num_pages, Hkv, page_size, D, dtype=torch.bfloat16, device=device)
+                         for _ in range(2)))
+        return cls(*(torch.empty(num_pages, Hkv, page_size, D // 2, dtype=torch.uint8, device=device)
+                     for _ in range(2)),
+                   *(torch.empty(num_pages, Hkv, page_size, 2, dtype=torch.bfloat16, device=device)
+                     for _ in range(2)))
+
+
+class KVBatch:
+    """A packed batch over a paged cache (fnl_kv_batch): cu_q int32 [B + 1], kv_len
+    int32 [B], block_table int32 [B, max_pages], all on the GPU, and max_q, the
+    caller's bound on any sequence's new tokens. The kernels read the arrays when
+    they run, so the object may be kept and its tensors updated in place."""
+
+    def __init__(self, cu_q, kv_len, block_table, max_q):
+        B = kv_len.shape[0]
+        _need(kv_len, "kv_len", (B,), torch.int32)
+        _need(cu_q, "cu_q", (B + 1,), torch.int32)
+        _need(block_table, "block_table", None, torch.int32)
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
+        self.cu_q, self.kv_len, self.block_table, self.max_q = cu_q, kv_len, block_table, int(max_q)
+        self.device = kv_len.device
+        if cu_q.device != self.device or block_table.device != self.device:
+            raise ValueError("cu_q, kv_len and block_table must be on one device")
+        self.c = _KvBatch(B, self.max_q, _p(cu_q), _p(kv_len), _p(block_table), block_table.shape[1])
+
+
+def _kv_stream(h, cache, batch, stream):
+    """The call's stream: `stream`, or the current one of the handle's device."""
+    if cache.device.index != h.device or batch.device.index != h.device:
+        raise ValueError(f"the cache and the batch must be on the handle's device, cuda:{h.device}")
+    return ctypes.c_void_p((torch.cuda.current_stream(h.device) if stream is None else stream).cuda_stream)
+
+
+def _kv_need(h, t, name, shape, dtype=torch.bfloat16):
+    _need(t, name, shape, dtype)
+    if t is not None and t.device.index != h.device:
+        raise ValueError(f"{name} must be on the handle's device, cuda:{h.device}")
+
+
+def rope_append_kv(h: Handle, cache: KVCache, batch: KVBatch, q, k, v, cos=None, sin=None, interleaved=False,
+                   q_out=None, stream=None):
+    """fnl_rope_append_kv. q [Hq, M, D], k and v [Hkv, M, D] (as add_norm_qkv returns
+    them), cos and sin fp32 [max_pos, rot_dim / 2]. k (rotated) and v go to their
+    pages; q_out (allocated when not given; may be q) gets the rotated q. Without
+    cos and sin nothing is rotated and q is returned as it is. Returns dict(q)."""
+    Hkv, D = cache.Hkv, cache.D
+    M = k.shape[1]
+    _kv_need(h, k, "k", (Hkv, M, D))
+    _kv_need(h, v, "v", (Hkv, M, D))
+    s = _kv_stream(h, cache, batch, stream)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin are given together")
+    if cos is None:
+        if q_out is not None:
+            raise ValueError("q_out is written by the rotation only: give cos and sin")
+        st = lib().fnl_rope_append_kv(h.ptr, s, cache.c, batch.c, M, 0, None, _p(k), _p(v), None, None, 0, 0, 0, None)
+    else:
+        _kv_need(h, q, "q", (q.shape[0], M, D))
+        if cos.dim() != 2:
+            raise ValueError("cos and sin must be [max_pos, rot_dim / 2]")
+        _kv_need(h, cos, "cos", cos.shape, torch.float32)
+        _kv_need(h, sin, "sin", cos.shape, torch.float32)
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        _kv_need(h, q_out, "q_out", q.shape)
+        st = lib().fnl_rope_append_kv(h.ptr, s, cache.c, batch.c, M, q.shape[0], _p(q), _p(k), _p(v), _p(cos), _p(sin),
+                                      2 * cos.shape[1], cos.shape[0], int(bool(interleaved)), _p(q_out))
+    if st != FNL_OK:
+        h._raise(st, "fnl_rope_append_kv")
+    return {"q": q if cos is None else q_out}
+
+
+def kv_gather(h: Handle, cache: KVCache, batch: KVBatch, M=None, k=None, v=None, stream=None):
+    """fnl_kv_gather: the batch's new tokens read back from their pages, k and v
+    bf16 [Hkv, M, D]. M (the packed rows) comes from k, or is given, or, when
+    neither is, read from cu_q, which waits for the device. Returns dict(k, v)."""
+    if k is not None or v is not None:
+        M = (v if k is None else k).shape[1]
+    elif M is None:
+        M = int(batch.cu_q[-1])
+    shape = (cache.Hkv, M, cache.D)
+    s = _kv_stream(h, cache, batch, stream)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+    _kv_need(h, k, "k", shape)
+    _kv_need(h, v, "v", shape)
+    st = lib().fnl_kv_gather(h.ptr, s, cache.c, batch.c, M, _p(k), _p(v))
+    if st != FNL_OK:
+        h._raise(st, "fnl_kv_gather")
+    return {"k": k, "v": v}
+
+
+def paged_attention(h: Handle, cache: KVCache, batch: KVBatch, q, scale=None, window=0, sinks=0, out=None, lse=None,
+                    stream=None):
+    """fnl_paged_attention: q [Hq, M, D] -> out [M, Hq * D], causal, with a sliding
+    window and `sinks` first tokens that stay visible when window > 0. scale
+    defaults to D ** -0.5; lse (fp32 [Hq, M]) is filled when given. Returns
+    dict(out, lse)."""
+    Hq, M, D = q.shape
+    _kv_need(h, q, "q", (Hq, M, cache.D))
+    s = _kv_stream(h, cache, batch, stream)
+    out = torch.empty(M, Hq * D, dtype=torch.bfloat16, device=q.device) if out is None else out
+    _kv_need(h, out, "out", (M, Hq * D))
+    _kv_need(h, lse, "lse", (Hq, M), torch.float32)
+    st = lib().fnl_paged_attention(h.ptr, s, cache.c, batch.c, M, Hq, _p(q), D ** -0.5 if scale is None else scale,
+                                   window, sinks, _p(out), _p(lse))
+    if st != FNL_OK:
+        h._raise(st, "fnl_paged_attention")
+    return {"out": out, "lse": lse}
 
 
 def run_workload(h: Handle, w, dev: dict, stats: bool = True, stream=None) -> dict:
