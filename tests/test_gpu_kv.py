@@ -485,3 +485,18 @@ def test_refusals(handle):
     left = torch.full((2, 4 * D), 7.0, dtype=torch.bfloat16, device="cuda")
     assert torch.all(att(handle, cache, none, q, out=left)["out"] == 7.0)
     handle.check()
+
+
+def test_a_wait_that_runs_out_is_reported(cuda_device):
+    """Fault injection: the first block withholds its first key tile; the call ends, check()
+    reports it, and the next call on the handle is right."""
+    h = fnl.Handle(0, wait_ns=50_000_000, debug_stall_calls=1)
+    c = Cache("bf16", [300, 200], 2, 128, 64, seed=50)
+    cache, tab = _dev(c)
+    batch = fnl.KVBatch(_cu([300, 200]), _i32(c.lens), tab, 300)
+    q = torch.randn(4, 500, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    fnl.paged_attention(h, cache, batch, q)
+    with pytest.raises(fnl.FnlError, match="status"):
+        h.check()
+    _check_attention(h, c, [300, 200], 4)
+    h.close()

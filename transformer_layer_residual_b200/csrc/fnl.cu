@@ -27,6 +27,7 @@
 #include "k5_tp.cuh"
 #include "k7_kv.cuh"
 #include "k8_attend.cuh"
+#include "k9_prompt.cuh"
 
 using fnl::bf16;
 using fnl::OpParams;
@@ -87,6 +88,19 @@ struct MapCache {
   }
 };
 
+// Encoded descriptors of paged caches (a loop calls with the same cache every step).
+struct PageMaps {
+  struct Entry {
+    const void* ptr;
+    long long rows, stride;
+    int pages, D, box;
+    CUtensorMap map;
+  };
+  static constexpr int kSize = 256;   // the k and v of 128 layers
+  std::vector<Entry> e;
+  int next = 0;
+};
+
 struct fnl_handle {
   int device = 0;
   int num_sms = 148;
@@ -105,6 +119,7 @@ struct fnl_handle {
   // Paged-cache calls: [status][arrival counters][partial sums], one fixed block
   // that never moves (a captured graph keeps its addresses).
   uint8_t* kv_ws = nullptr;
+  PageMaps page_maps;
 };
 
 namespace {
@@ -1503,6 +1518,74 @@ fnl_status append_launch(fnl_handle* h, bool interleaved, dim3 grid, cudaStream_
   return kv_launch(h, fnl::k7_append<D, FMT, false>, grid, fnl::kKvThreads, 0, s, p);
 }
 
+// One (page, head)'s rows of bf16 pages, `box` rows of 64 values at a time with the
+// 128-byte swizzle: dimensions (value, row of the page over its heads, page).
+fnl_status page_map(fnl_handle* h, CUtensorMap* m, const KvParams& kv, const void* ptr, int D) {
+  const long long rows = static_cast<long long>(kv.Hkv) << kv.page_shift;
+  const int box = std::min(1 << kv.page_shift, fnl::k9::TILE);
+  for (const auto& x : h->page_maps.e)
+    if (x.ptr == ptr && x.rows == rows && x.stride == kv.page_stride && x.pages == kv.num_pages && x.D == D && x.box == box) {
+      *m = x.map;
+      return FNL_OK;
+    }
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(std::max(kv.num_pages, 1))};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(kv.page_stride)};
+  cuuint32_t boxd[3] = {64, static_cast<cuuint32_t>(box), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, boxd, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(h, FNL_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  PageMaps& t = h->page_maps;
+  const PageMaps::Entry x{ptr, rows, kv.page_stride, kv.num_pages, D, box, *m};
+  if (static_cast<int>(t.e.size()) < PageMaps::kSize) t.e.push_back(x);
+  else t.e[t.next] = x;
+  t.next = (t.next + 1) % PageMaps::kSize;
+  return FNL_OK;
+}
+
+template <int D>
+fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a) {
+  using namespace fnl::k9;
+  fnl_status st = get_encoder(h);
+  if (st != FNL_OK) return st;
+  CUtensorMap mk, mv;
+  if ((st = page_map(h, &mk, a.kv, a.kv.k, D)) != FNL_OK || (st = page_map(h, &mv, a.kv, a.kv.v, D)) != FNL_OK) return st;
+  if ((st = set_smem(h, k9_prompt<D>, Cfg<D>::SMEM)) != FNL_OK) return st;
+  // the warps' register shares must fit what the block is launched with, or its warps would wait for them forever
+  static const int regs = [] {
+    cudaFuncAttributes fa{};
+    return cudaFuncGetAttributes(&fa, k9_prompt<D>) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs * THREADS < 256 * REG_SOFTMAX + 128 * REG_OTHER)
+    return fail(h, FNL_ERR_UNSUPPORTED, "the paged attention kernel was built with %d registers a thread", regs);
+  Params p{};
+  p.a = a;
+  p.wait_ns = h->opt.wait_ns > 0 ? static_cast<unsigned long long>(h->opt.wait_ns) : FNL_WAIT_NS;
+  if (h->opt.debug_stall_calls > 0) {   // fault injection for the status-path tests
+    p.stall = 1;
+    --h->opt.debug_stall_calls;
+  }
+  const long long tiles = (static_cast<long long>(a.kv.max_q) * a.group + ROWS - 1) / ROWS;
+  char buf[160];
+  snprintf(buf, sizeof(buf), "paged attention, tensor-core form, grid %lld x %d x %d", tiles, a.kv.Hkv, a.kv.B);
+  h->plan_text = buf;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles), a.kv.Hkv, a.kv.B);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = Cfg<D>::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k9_prompt<D>, mk, mv, p);
+  if (e != cudaSuccess) return cuda_fail(h, e, "launch of the paged attention kernel");
+  return FNL_OK;
+}
+
 template <int D, int FMT>
 fnl_status attend_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p) {
   char buf[160];
@@ -1514,6 +1597,7 @@ fnl_status attend_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p
     h->plan_text = buf;
     return kv_launch(h, fnl::k8::k8_attend_split<D, FMT>, dim3(grid), C::THREADS, C::SMEM, s, p);
   }
+  if (FMT == fnl::kKvBf16) return prompt_launch<D>(h, s, p);
   typedef fnl::k8::RowsCfg<D, FMT> C;
   const long long tiles = (static_cast<long long>(p.kv.max_q) * p.group + C::ROWS - 1) / C::ROWS;
   if (tiles > 0x7fffffffLL) return fail(h, FNL_ERR_UNSUPPORTED, "max_q * Hq / Hkv is too large");
