@@ -318,8 +318,8 @@ fnl_status fnl_linear_add_residual(fnl_handle* h, fnl_stream stream, const fnl_b
  * c = round((x - lo) / s) (to nearest even, in fp32; 0 where s = 0): every value
  * is within s / 2 of what its code stands for. Rows have to be finite.
  * Pages may lie apart: page_stride bytes from page to page in k and in v (0:
- * dense; a multiple of 16), scale_page_stride in the scales (0: dense), so that k
- * and v may be the halves of one [num_pages, 2, ...] allocation. */
+ * dense), scale_page_stride in the scales (0: dense), both multiples of 16, so that
+ * k and v may be the halves of one [num_pages, 2, ...] allocation. */
 typedef enum { FNL_KV_BF16 = 0, FNL_KV_INT4 = 1 } fnl_kv_format;
 
 typedef struct {
@@ -371,7 +371,7 @@ typedef struct {
  * coded when the cache is FNL_KV_INT4 (k from its rotated bf16 values).
  * rot_dim = 0: no rotation; q, q_out, cos and sin must then be NULL. One kernel.
  * Errors: FNL_ERR_INVALID_ARG, FNL_ERR_ALIGNMENT (16 bytes for tensors, 4 for
- * integer lists and scales), FNL_ERR_ALIAS (q_out partly on q, or a tensor on the
+ * integer lists), FNL_ERR_ALIAS (q_out partly on q, or a tensor on the
  * cache), FNL_ERR_UNSUPPORTED (D, page_size, B > 65535). */
 fnl_status fnl_rope_append_kv(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch,
                               int M, int Hq, const fnl_bf16* q, const fnl_bf16* k, const fnl_bf16* v,

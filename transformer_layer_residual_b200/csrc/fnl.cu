@@ -27,6 +27,7 @@
 #include "k5_tp.cuh"
 #include "k7_kv.cuh"
 #include "k8_attend.cuh"
+#include "k8_rows.cuh"
 #include "k9_prompt.cuh"
 
 using fnl::bf16;
@@ -1421,8 +1422,8 @@ fnl_status kv_params(fnl_handle* h, const fnl_kv_cache* c, const fnl_kv_batch* b
   if (page_rows > 0x7fffffffLL) return fail(h, FNL_ERR_UNSUPPORTED, "Hkv * page_size must stay below 2^31");
   if (stride < page_rows * row_bytes || (int4 && sstride < page_rows * 4))
     return fail(h, FNL_ERR_INVALID_ARG, "a page stride is smaller than a page");
-  if (stride % 16 || (int4 && sstride % 4))
-    return fail(h, FNL_ERR_ALIGNMENT, "page_stride must be a multiple of 16 bytes, scale_page_stride of 4");
+  if (stride % 16 || (int4 && sstride % 16))
+    return fail(h, FNL_ERR_ALIGNMENT, "page strides must be multiples of 16 bytes");
   p->k = static_cast<uint8_t*>(c->k);
   p->v = static_cast<uint8_t*>(c->v);
   p->k_scale = reinterpret_cast<uint32_t*>(c->k_scale);
@@ -1447,10 +1448,11 @@ fnl_status kv_params(fnl_handle* h, const fnl_kv_cache* c, const fnl_kv_batch* b
     return fail(h, FNL_ERR_INVALID_ARG, "k_scale and v_scale must be NULL for bf16 pages");
   if (!b->cu_q || !b->kv_len || !b->block_table)
     return fail(h, FNL_ERR_INVALID_ARG, "cu_q, kv_len and block_table are required");
-  if (!al16(c->k) || !al16(c->v)) return fail(h, FNL_ERR_ALIGNMENT, "k and v must be 16-byte aligned");
-  const void* p4[] = {c->k_scale, c->v_scale, b->cu_q, b->kv_len, b->block_table};
+  if (!al16(c->k) || !al16(c->v) || !al16(c->k_scale) || !al16(c->v_scale))
+    return fail(h, FNL_ERR_ALIGNMENT, "the cache's k, v, k_scale and v_scale must be 16-byte aligned");
+  const void* p4[] = {b->cu_q, b->kv_len, b->block_table};
   for (const void* q : p4)
-    if (q && !al4(q)) return fail(h, FNL_ERR_ALIGNMENT, "scales, cu_q, kv_len and block_table must be 4-byte aligned");
+    if (!al4(q)) return fail(h, FNL_ERR_ALIGNMENT, "cu_q, kv_len and block_table must be 4-byte aligned");
   p->status = reinterpret_cast<int*>(h->kv_ws);
   cudaError_t e = cudaSetDevice(h->device);
   if (e != cudaSuccess) return cuda_fail(h, e, "cudaSetDevice");
@@ -1562,7 +1564,6 @@ fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a
     return fail(h, FNL_ERR_UNSUPPORTED, "the paged attention kernel was built with %d registers a thread", regs);
   Params p{};
   p.a = a;
-  p.wait_ns = h->opt.wait_ns > 0 ? static_cast<unsigned long long>(h->opt.wait_ns) : FNL_WAIT_NS;
   if (h->opt.debug_stall_calls > 0) {   // fault injection for the status-path tests
     p.stall = 1;
     --h->opt.debug_stall_calls;
@@ -1586,17 +1587,23 @@ fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a
   return FNL_OK;
 }
 
+template <int D, int FMT, int NR>
+fnl_status split_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p) {
+  typedef fnl::k8::SplitCfg<D, FMT, NR> C;
+  static_assert(C::BLOCKS <= kKvBlocksPerSm, "workspace slots per SM");
+  const int grid = h->num_sms * C::BLOCKS;
+  char buf[160];
+  snprintf(buf, sizeof(buf), "paged attention, split form, %d rows, grid %d", C::ROWS, grid);
+  h->plan_text = buf;
+  return kv_launch(h, fnl::k8::k8_attend_split<D, FMT, NR>, dim3(grid), C::THREADS, C::SMEM, s, p);
+}
+
 template <int D, int FMT>
 fnl_status attend_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p) {
   char buf[160];
-  if (static_cast<long long>(p.kv.max_q) * p.group <= fnl::k8::kRowsMax) {
-    typedef fnl::k8::SplitCfg<D, FMT> C;
-    static_assert(C::BLOCKS <= kKvBlocksPerSm, "workspace slots per SM");
-    const int grid = h->num_sms * C::BLOCKS;
-    snprintf(buf, sizeof(buf), "paged attention, split form, grid %d", grid);
-    h->plan_text = buf;
-    return kv_launch(h, fnl::k8::k8_attend_split<D, FMT>, dim3(grid), C::THREADS, C::SMEM, s, p);
-  }
+  const long long rows = static_cast<long long>(p.kv.max_q) * p.group;
+  if (rows <= 8) return split_launch<D, FMT, 1>(h, s, p);
+  if (rows <= 16) return split_launch<D, FMT, 2>(h, s, p);
   if (FMT == fnl::kKvBf16) return prompt_launch<D>(h, s, p);
   typedef fnl::k8::RowsCfg<D, FMT> C;
   const long long tiles = (static_cast<long long>(p.kv.max_q) * p.group + C::ROWS - 1) / C::ROWS;
@@ -1700,6 +1707,7 @@ fnl_status fnl_paged_attention(fnl_handle* h, fnl_stream stream, const fnl_kv_ca
   p.Hq = Hq; p.group = Hq / cache->Hkv;
   p.scale_log2 = scale * 1.44269504088896340736f;
   p.window = window; p.sinks = sinks;
+  p.wait_ns = h->opt.wait_ns > 0 ? static_cast<unsigned long long>(h->opt.wait_ns) : FNL_WAIT_NS;
   p.counters = reinterpret_cast<unsigned*>(h->kv_ws + kStatusBytes);
   p.part = reinterpret_cast<float*>(h->kv_ws + kv_part_offset(h));
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -1,30 +1,30 @@
-// K8: attention over the paged cache, softmax(scale q k^T) v with a causal
-// mask, a sliding window and first tokens that stay visible.
+// K8: attention of a few new tokens over the paged cache, softmax(scale q k^T) v
+// with a causal mask, a sliding window and first tokens that stay visible.
 //
 // One pass over the keys with the running maximum and sum of the softmax
 // (base 2: the scores carry scale * log2 e). The rows of a sequence and key head
 // are its new tokens times the `group` query heads that share that head, token
-// by token: row r is token r / group, head r % group. So one query token of a
-// grouped model still fills the 16 rows of an m16n8k16 product, and every key
-// and value row is read once for all of them.
+// by token: row r is token r / group, head r % group. Every key and value row is
+// read once for all of them.
 //
-// Two forms of the same arithmetic:
-//   split  few rows (a decode step, a few draft tokens). HBM bound: the keys and
-//          values are read once, at 2 * rows products per element, far below
-//          what the tensor pipe can do, so the register-level mma form is used:
-//          scores and probabilities stay in registers and no accumulator makes a
-//          round trip through tensor memory. Each warp streams its own keys
-//          through its own ring of asynchronous copies and keeps its own softmax
-//          state, so the main loop has no block barrier. The (sequence, key head,
-//          key tile) units of the whole batch are dealt evenly over the blocks,
-//          so ragged lengths cost nothing; a block's first and last pieces may
-//          share their rows with other blocks, which leave fp32 partial sums
-//          that the last one to arrive adds in block order (results do not
-//          depend on the order of arrival).
-//   rows   many rows: each warp owns 16 of the block's rows, all warps read the
-//          same key tile.
+// HBM bound: the keys and values are read once, with 2 * rows products per
+// element, far below what the tensor pipe can do. So the register-level mma form
+// is used, keys as the 16-row operand and the rows as its 8 columns: S^T = K Q^T
+// and O^T = V^T P^T. Scores and probabilities stay in registers (P^T is S^T's
+// fragment transposed lane by lane), a decode step of up to 8 heads per key head
+// wastes no half tile, and a key or value fragment is unpacked once for all rows.
 //
-// 4-bit pages: a code enters the product as the exact bf16 value 128 + code
+// Each warp streams its own keys through its own ring of asynchronous copies (bf16
+// pages: 16 bytes a lane, swizzled for ldmatrix; 4-bit pages: bulk copies of whole
+// runs of rows, whose few instructions leave the issue slots to the unpacking) and
+// keeps its own softmax state, so the main loop has no block barrier. The
+// (sequence, key head, key tile) units of the whole batch are dealt evenly over
+// the blocks, so ragged lengths cost nothing; a block's first and last pieces may
+// share their rows with other blocks, which leave fp32 partial sums that the last
+// one to arrive adds in block order (results do not depend on the order of
+// arrival).
+//
+// 4-bit pages: a key's code enters the product as the exact bf16 value 128 + code
 // (two bit operations for two codes); the row's scale and minimum are applied to
 // the score, s (q . c) + (m - 128 s) sum(q), in fp32. For the values, code - 8
 // is formed exactly in bf16 (centred, so that the sum over many keys keeps its
@@ -32,8 +32,8 @@
 // end. Neither keys nor values are ever rounded.
 //
 // Rounding: the probabilities enter the second product as bf16 (relative error
-// 2^-8 at most each, the same size as the output's own rounding); their sum is taken in
-// fp32 before that rounding.
+// 2^-8 at most each, the same size as the output's own rounding); their sum is
+// taken in fp32 before that rounding.
 //
 // Keys that no row may see (behind the sequence's end, before the window) are
 // never read: their copies write zeros, so what such slots hold, NaN included,
@@ -52,12 +52,15 @@ struct AttnParams {
   int Hq, group;
   float scale_log2;   // scale * log2(e)
   int window, sinks;  // window 0: none
+  unsigned long long wait_ns;   // limit of the waits for copies
   float* part;        // split form: [2 * blocks][kPartFloats]
   unsigned* counters; // split form: [blocks], zero between launches
 };
 
 namespace k8 {
 
+constexpr float kGrowth = 8.f;   // accumulators are rescaled when a row's maximum (base 2) has grown by more: the
+                                 // probabilities stay below 256, which bf16 and fp32 hold as exactly as below 1
 constexpr int kRowsMax = 16;                                   // rows of one piece of the split form
 constexpr int kPartFloats = kRowsMax * (128 + 2);              // accumulators, maximum, sum
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -69,9 +72,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -91,14 +91,30 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
                : "memory");
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(   // not volatile: independent products may be interleaved
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
       "%2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// 8 x 8 matrix of 16-bit values, a row over four lanes: transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// The wait that an aborting role ends with: bounded, records nothing.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > FNL_WAIT_NS) return;
+}
 // two codes at bits 0-3 and 16-19 -> bf16 pair 128 + code
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) { return (w & 0x000F000Fu) | 0x43004300u; }
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  uint32_t r;   // (w & mask) | 128.0 in one instruction
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(0x000F000Fu), "r"(0x43004300u));
+  return r;
+}
 // the same, centred: code - 8 (exact)
 __device__ __forceinline__ uint32_t code_pair8(uint32_t w) {
   uint32_t r;
@@ -106,26 +122,19 @@ __device__ __forceinline__ uint32_t code_pair8(uint32_t w) {
   return r;
 }
 
-// Layout of one warp step (split form) or one block tile (rows form) of KEYS
-// keys in shared memory.
+// Layout of one warp step of KEYS keys in shared memory: key rows, value rows,
+// then (4-bit) the scale pairs of both.
 template <int D, int FMT, int KEYS>
 struct Tile {
-  // bf16: rows of D values, 16-byte chunks XORed with the row number (ldmatrix
-  // reads 8 rows of one chunk). 4-bit: key rows packed; value rows at a pitch
-  // whose even rows fall on distinct banks (a lane reads words of rows 2t, 2t+1).
-  static constexpr int kKRow = FMT == kKvBf16 ? D * 2 : D / 2;
-  static constexpr int kVRow = FMT == kKvBf16 ? D * 2 : (D == 128 ? 80 : 48);
-  static constexpr int kV = KEYS * kKRow;
-  static constexpr int kKs = kV + KEYS * kVRow;            // 4-bit: scale pairs of the keys, then of the values
-  static constexpr int kVs = kKs + (FMT == kKvBf16 ? 0 : KEYS * 4);
-  static constexpr int kBytes = kVs + (FMT == kKvBf16 ? 0 : KEYS * 4);
-  static constexpr int kChunks = (FMT == kKvBf16 ? D * 2 : D / 2) / 16;   // 16-byte chunks of a row
-
-  static __device__ __forceinline__ uint32_t k_chunk(int row, int c) {
-    return FMT == kKvBf16 ? row * kKRow + ((c ^ (row & 7)) << 4) : row * kKRow + (c << 4);
-  }
-  static __device__ __forceinline__ uint32_t v_chunk(int row, int c) {
-    return FMT == kKvBf16 ? kV + row * kVRow + ((c ^ (row & 7)) << 4) : kV + row * kVRow + (c << 4);
+  static constexpr int kRow = FMT == kKvBf16 ? D * 2 : D / 2;
+  static constexpr int kV = KEYS * kRow;
+  static constexpr int kKs = 2 * kV;
+  static constexpr int kVs = kKs + KEYS * 4;
+  static constexpr int kBytes = FMT == kKvBf16 ? kKs : kVs + KEYS * 4;
+  static constexpr int kChunks = kRow / 16;   // 16-byte chunks of a row
+  // bf16 chunks are XORed with the row number: ldmatrix reads one chunk of 8 rows
+  static __device__ __forceinline__ uint32_t chunk(int row, int c) {
+    return row * kRow + ((FMT == kKvBf16 ? c ^ (row & 7) : c) << 4);
   }
 };
 
@@ -147,241 +156,278 @@ struct Sight {
   }
 };
 
-// Softmax state and accumulators of 16 rows held by one warp (rows g and g + 8
-// of each lane's quad), and the step over NT * 8 keys in shared memory.
-template <int D, int FMT, int NT>
-struct Rows16 {
-  static constexpr int kQ = D / 16;
-  uint32_t q[kQ][4];
-  float o[D / 8][4];
-  float m0, m1, l0, l1;
-  float qs0, qs1;      // 4-bit: sum of the row's q
-  float c0, c1;        // 4-bit: sum of p (minimum + 8 scale)
-  int p0, p1;          // positions of the two rows' tokens
+// Softmax state and accumulators of NR * 8 rows held by one warp, and the step
+// over KEYS keys in shared memory. Lane (g, t) = (lane / 4, lane % 4) holds, of each
+// 8 rows, rows 2t and 2t + 1: scores of the keys g, g + 8, .. and accumulators of
+// the d that its mma rows g and g + 8 stand for.
+template <int D, int FMT, int NR, int KEYS>
+struct RowState {
+  static constexpr int KQ = D / 16, KT = KEYS / 16;
+  uint32_t q[KQ][NR][2];
+  float o[KQ][NR][4];
+  float m[NR][2], l[NR][2];
+  float qs[NR][2];     // 4-bit: sum of the row's q
+  float cm[NR][2];     // 4-bit: sum of p (minimum + 8 scale)
+  int pos[NR][2];      // positions of the rows' tokens
 
-  __device__ __forceinline__ void reset() {
-    m0 = m1 = -INFINITY;
-    l0 = l1 = c0 = c1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  // Key of mma row r (0..15) of a 16-key tile. 4-bit: a permutation that puts the
+  // value rows that a lane quad reads together on both halves of the banks.
+  static __device__ __forceinline__ int key_of_row(int r) {
+    return FMT == kKvBf16 ? r : (r & 8) + ((r & 7) >> 1) + 4 * (r & 1);
+  }
+  // d of accumulator rows g (h = 0) and g + 8 (h = 1) of tile i
+  static __device__ __forceinline__ int d_of(int i, int h) {
+    const int g = (threadIdx.x & 31) >> 2;
+    if (FMT == kKvBf16) return i * 16 + h * 8 + g;
+    return D == 128 ? 16 * g + 8 * h + i : 8 * g + 4 * h + i;
   }
 
-  // q row pointers of rows g and g + 8 (null: an empty row of zeros)
-  __device__ __forceinline__ void load_q(const bf16* r0, const bf16* r1) {
+  // q rows g of each 8 (null: an empty row of zeros) as the column operand
+  __device__ __forceinline__ void load(const bf16* (&r)[NR]) {
     const int t = threadIdx.x & 3;
-    auto pair = [](const bf16* r, int a, int b) -> uint32_t {
-      if (!r) return 0u;
-      return static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(r) + a)) |
-             (static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(r) + b)) << 16);
-    };
-    if (FMT == kKvBf16) {
 #pragma unroll
-      for (int s = 0; s < kQ; ++s) {
-        const int a = s * 16 + 2 * t;
-        q[s][0] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(r0 + a)) : 0u;
-        q[s][1] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(r1 + a)) : 0u;
-        q[s][2] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(r0 + a + 8)) : 0u;
-        q[s][3] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(r1 + a + 8)) : 0u;
-      }
-    } else {
-      // word j of a lane's codes holds d = (D / 4) t + 8 j + 0..7; product step
-      // (j, half) pairs codes (0, 4) and (1, 5), or (2, 6) and (3, 7), as they
-      // come out of the word by shifts, and q follows that order of d
+    for (int n = 0; n < NR; ++n) {
 #pragma unroll
-      for (int s = 0; s < kQ; ++s) {
-        const int d = (D / 4) * t + 8 * (s >> 1) + 2 * (s & 1);
-        q[s][0] = pair(r0, d, d + 4);
-        q[s][1] = pair(r1, d, d + 4);
-        q[s][2] = pair(r0, d + 1, d + 5);
-        q[s][3] = pair(r1, d + 1, d + 5);
+      for (int s = 0; s < KQ; ++s) {
+        if (FMT == kKvBf16) {
+          const int a = s * 16 + 2 * t;
+          q[s][n][0] = r[n] ? __ldg(reinterpret_cast<const uint32_t*>(r[n] + a)) : 0u;
+          q[s][n][1] = r[n] ? __ldg(reinterpret_cast<const uint32_t*>(r[n] + a + 8)) : 0u;
+        } else {
+          // word j of a lane's codes holds d = (D / 4) t + 8 j + 0..7; product step
+          // (j, half) pairs codes (0, 4) and (1, 5), or (2, 6) and (3, 7), as they
+          // come out of the word by shifts, and q follows that order of d
+          const int d = (D / 4) * t + 8 * (s >> 1) + 2 * (s & 1);
+          const uint16_t* x = reinterpret_cast<const uint16_t*>(r[n]);
+          q[s][n][0] = x ? __ldg(x + d) | (static_cast<uint32_t>(__ldg(x + d + 4)) << 16) : 0u;
+          q[s][n][1] = x ? __ldg(x + d + 1) | (static_cast<uint32_t>(__ldg(x + d + 5)) << 16) : 0u;
+        }
       }
-      qs0 = qs1 = 0.f;
+      if (FMT == kKvInt4) {
+        float a = 0.f;
 #pragma unroll
-      for (int s = 0; s < kQ; ++s) {
-        qs0 += bf_lo(q[s][0]) + bf_hi(q[s][0]) + bf_lo(q[s][2]) + bf_hi(q[s][2]);
-        qs1 += bf_lo(q[s][1]) + bf_hi(q[s][1]) + bf_lo(q[s][3]) + bf_hi(q[s][3]);
+        for (int s = 0; s < KQ; ++s) a += bf_lo(q[s][n][0]) + bf_hi(q[s][n][0]) + bf_lo(q[s][n][1]) + bf_hi(q[s][n][1]);
+        a += __shfl_xor_sync(0xffffffffu, a, 1);
+        a += __shfl_xor_sync(0xffffffffu, a, 2);
+        qs[n][0] = __shfl_sync(0xffffffffu, a, 8 * t);       // rows 2t and 2t + 1
+        qs[n][1] = __shfl_sync(0xffffffffu, a, 8 * t + 4);
       }
-      qs0 += __shfl_xor_sync(0xffffffffu, qs0, 1);
-      qs1 += __shfl_xor_sync(0xffffffffu, qs1, 1);
-      qs0 += __shfl_xor_sync(0xffffffffu, qs0, 2);
-      qs1 += __shfl_xor_sync(0xffffffffu, qs1, 2);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[n][e] = -INFINITY;
+        l[n][e] = cm[n][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < KQ; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     }
   }
 
-  // Keys [key, key + 8 NT) whose rows start at row `row` of the tile at `base`.
-  template <int KEYS>
-  __device__ __forceinline__ void step(uint32_t base, int row, int key, const Sight& sight, float scale_log2) {
+  // Keys [key, key + KEYS) at shared address `base`.
+  __device__ __forceinline__ void step(uint32_t base, int key, const Sight& sight, float scale_log2) {
     typedef Tile<D, FMT, KEYS> T;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float s[NT][4];
+    float s[KT][NR][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int n = 0; n < NR; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = 0.f;
     // ---- scores
     if (FMT == kKvBf16) {
 #pragma unroll
-      for (int kk = 0; kk < kQ; ++kk) {
+      for (int kk = 0; kk < KQ; ++kk) {
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          uint32_t b[4];
-          ldsm4(b, base + T::k_chunk(row + n * 8 + ((lane >> 4) << 3) + (lane & 7), kk * 2 + ((lane >> 3) & 1)));
-          mma(s[n], q[kk], b[0], b[1]);
-          mma(s[n + 1], q[kk], b[2], b[3]);
+        for (int i = 0; i < KT; ++i) {
+          uint32_t a[4];
+          ldsm4(a, base + T::chunk(i * 16 + (lane & 15), kk * 2 + (lane >> 4)));
+#pragma unroll
+          for (int n = 0; n < NR; ++n) mma(s[i][n], a, q[kk][n][0], q[kk][n][1]);
         }
       }
     } else {
+      uint32_t w[KT][2][D / 32];   // this lane's codes of the keys of rows g and g + 8
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint32_t a = base + (row + n * 8 + g) * T::kKRow + t * (D / 8);
-        uint32_t w[D / 32];
-        if (D == 128) {
-          const uint4 x = ld_shared_v4(a);
-          w[0] = x.x; w[1] = x.y; w[D / 32 - 2] = x.z; w[D / 32 - 1] = x.w;
-        } else {
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
-        }
+      for (int i = 0; i < KT; ++i) {
+        const uint32_t at = base + (i * 16 + key_of_row(g)) * T::kRow + t * (D / 8);
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          mma(s[n], q[2 * j], code_pair(w[j]), code_pair(w[j] >> 4));
-          mma(s[n], q[2 * j + 1], code_pair(w[j] >> 8), code_pair(w[j] >> 12));
+        for (int h = 0; h < 2; ++h) {
+          if (D == 128) {
+            const uint4 x = ld_shared_v4(at + h * 8 * T::kRow);
+            w[i][h][0] = x.x; w[i][h][1] = x.y; w[i][h][D / 32 - 2] = x.z; w[i][h][D / 32 - 1] = x.w;
+          } else {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i][h][0]), "=r"(w[i][h][1]) : "r"(at + h * 8 * T::kRow));
+          }
         }
       }
-    }
-    float vs[NT][2], vm[NT][2];   // 4-bit: scale of the value rows, minimum + 8 scale
-    if (FMT == kKvInt4) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        uint32_t x, y;
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(base + T::kKs + (row + n * 8 + 2 * t) * 4));
-        const float sx = kv_scale_of(x), sy = kv_scale_of(y);
-        const float mx = fmaf(-128.f, sx, kv_min_of(x)), my = fmaf(-128.f, sy, kv_min_of(y));
-        s[n][0] = fmaf(sx, s[n][0], mx * qs0);
-        s[n][1] = fmaf(sy, s[n][1], my * qs0);
-        s[n][2] = fmaf(sx, s[n][2], mx * qs1);
-        s[n][3] = fmaf(sy, s[n][3], my * qs1);
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(base + T::kVs + (row + n * 8 + 2 * t) * 4));
-        vs[n][0] = kv_scale_of(x);
-        vs[n][1] = kv_scale_of(y);
-        vm[n][0] = fmaf(8.f, vs[n][0], kv_min_of(x));
-        vm[n][1] = fmaf(8.f, vs[n][1], kv_min_of(y));
-      }
-    }
-    // ---- masks, only where some row does not see some key
-    if (!sight.all(key, NT * 8)) {
+      for (int j = 0; j < D / 32; ++j) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+        for (int f = 0; f < 2; ++f) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = key + n * 8 + 2 * t + e;
-          if (!sight.sees(p0, j)) s[n][e] = -INFINITY;
-          if (!sight.sees(p1, j)) s[n][2 + e] = -INFINITY;
-        }
-      }
-    }
-    // ---- running maximum
-    float x0 = s[0][0], x1 = s[0][2];
+          for (int i = 0; i < KT; ++i) {
+            const uint32_t a[4] = {code_pair(w[i][0][j] >> (8 * f)), code_pair(w[i][1][j] >> (8 * f)),
+                                   code_pair(w[i][0][j] >> (8 * f + 4)), code_pair(w[i][1][j] >> (8 * f + 4))};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      x0 = fmaxf(x0, fmaxf(s[n][0], s[n][1]));
-      x1 = fmaxf(x1, fmaxf(s[n][2], s[n][3]));
-    }
-    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2)) * scale_log2;
-    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2)) * scale_log2;
-    if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
-      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-      const float f0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), f1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
-      m0 = n0;
-      m1 = n1;
-      l0 *= f0;
-      l1 *= f1;
-      if (FMT == kKvInt4) {
-        c0 *= f0;
-        c1 *= f1;
-      }
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][0] *= f0;
-        o[i][1] *= f0;
-        o[i][2] *= f1;
-        o[i][3] *= f1;
-      }
-    }
-    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-    // ---- probabilities, and the second product
-#pragma unroll
-    for (int j = 0; j < NT / 2; ++j) {
-      uint32_t a[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int n = 2 * j + h;
-        float e0 = ex2(fmaf(s[n][0], scale_log2, -b0)), e1 = ex2(fmaf(s[n][1], scale_log2, -b0));
-        float e2 = ex2(fmaf(s[n][2], scale_log2, -b1)), e3 = ex2(fmaf(s[n][3], scale_log2, -b1));
-        l0 += e0 + e1;
-        l1 += e2 + e3;
-        if (FMT == kKvInt4) {
-          c0 = fmaf(e0, vm[n][0], fmaf(e1, vm[n][1], c0));
-          c1 = fmaf(e2, vm[n][0], fmaf(e3, vm[n][1], c1));
-          e0 *= vs[n][0]; e1 *= vs[n][1]; e2 *= vs[n][0]; e3 *= vs[n][1];
-        }
-        a[2 * h] = pack_bf16x2(e0, e1);
-        a[2 * h + 1] = pack_bf16x2(e2, e3);
-      }
-      if (FMT == kKvBf16) {
-#pragma unroll
-        for (int i = 0; i < D / 8; i += 2) {
-          uint32_t b[4];
-          ldsm4t(b, base + T::v_chunk(row + j * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), i + (lane >> 4)));
-          mma(o[i], a, b[0], b[1]);
-          mma(o[i + 1], a, b[2], b[3]);
-        }
-      } else {
-        const uint32_t v = base + T::kV + (row + j * 16 + 2 * t) * T::kVRow + g * 4;
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w) {
-          uint32_t x[4];   // word g + 8 w of the rows 2t, 2t + 1, 2t + 8, 2t + 9
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[0]) : "r"(v + w * 32));
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[1]) : "r"(v + w * 32 + T::kVRow));
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[2]) : "r"(v + w * 32 + 8 * T::kVRow));
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[3]) : "r"(v + w * 32 + 9 * T::kVRow));
-          // neighbouring rows side by side: codes i and i of both for i = 0..3, then 4..7
-          const uint32_t a0 = __byte_perm(x[0], x[1], 0x5410), a1 = __byte_perm(x[0], x[1], 0x7632);
-          const uint32_t d0 = __byte_perm(x[2], x[3], 0x5410), d1 = __byte_perm(x[2], x[3], 0x7632);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {   // tile i of word w: column g is d = 8 (g + 8 w) + i
-            mma(o[w * 8 + i], a, code_pair8(a0 >> (4 * i)), code_pair8(d0 >> (4 * i)));
-            mma(o[w * 8 + 4 + i], a, code_pair8(a1 >> (4 * i)), code_pair8(d1 >> (4 * i)));
+            for (int n = 0; n < NR; ++n) mma(s[i][n], a, q[2 * j + f][n][0], q[2 * j + f][n][1]);
           }
         }
       }
     }
-  }
-
-  // Sums of the quad's lanes; the 4-bit minimum term joins the accumulators.
-  __device__ __forceinline__ void finish() {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    float vs[KT][2], vm[KT][2];   // 4-bit: scale of this lane's value rows, minimum + 8 scale
+    const bool edge = !sight.all(key, KEYS);
     if (FMT == kKvInt4) {
-      c0 += __shfl_xor_sync(0xffffffffu, c0, 1);
-      c1 += __shfl_xor_sync(0xffffffffu, c1, 1);
-      c0 += __shfl_xor_sync(0xffffffffu, c0, 2);
-      c1 += __shfl_xor_sync(0xffffffffu, c1, 2);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][0] += c0;
-        o[i][1] += c0;
-        o[i][2] += c1;
-        o[i][3] += c1;
+      for (int i = 0; i < KT; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = i * 16 + h * 8 + key_of_row(g);
+          uint32_t x, y;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(base + T::kKs + j * 4));
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y) : "r"(base + T::kVs + j * 4));
+          const float sx = kv_scale_of(x), mx = fmaf(-128.f, sx, kv_min_of(x));
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            s[i][n][2 * h] = fmaf(sx, s[i][n][2 * h], mx * qs[n][0]);
+            s[i][n][2 * h + 1] = fmaf(sx, s[i][n][2 * h + 1], mx * qs[n][1]);
+          }
+          vs[i][h] = kv_scale_of(y);
+          vm[i][h] = fmaf(8.f, vs[i][h], kv_min_of(y));
+        }
+      }
+    }
+    // ---- masks, only where some row does not see some key
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = key + i * 16 + h * 8 + key_of_row(g);
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!sight.sees(pos[n][e], j)) s[i][n][2 * h + e] = -INFINITY;
+          if (FMT == kKvInt4 && !sight.any(j)) vs[i][h] = vm[i][h] = 0.f;   // such slots may hold anything
+        }
+    }
+    // ---- running maximum
+    float x[NR][2];
+    bool grow = false;
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float y = fmaxf(s[0][n][e], s[0][n][2 + e]);
+#pragma unroll
+        for (int i = 1; i < KT; ++i) y = fmaxf(y, fmaxf(s[i][n][e], s[i][n][2 + e]));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16)) * scale_log2;
+        x[n][e] = y;
+        grow |= y > m[n][e] + kGrowth;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool up = x[n][e] > m[n][e] + kGrowth;
+          const float f = up ? ex2(m[n][e] - x[n][e]) : 1.f;
+          if (up) m[n][e] = x[n][e];
+          l[n][e] *= f;
+          cm[n][e] *= f;
+#pragma unroll
+          for (int i = 0; i < KQ; ++i) {
+            o[i][n][e] *= f;
+            o[i][n][2 + e] *= f;
+          }
+        }
+    }
+    // ---- probabilities, transposed into the second product's column operand
+    uint32_t pb[KT][NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const float b0 = m[n][0] == -INFINITY ? 0.f : m[n][0], b1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float e0 = ex2(fmaf(s[i][n][2 * h], scale_log2, -b0)), e1 = ex2(fmaf(s[i][n][2 * h + 1], scale_log2, -b1));
+          l[n][0] += e0;
+          l[n][1] += e1;
+          if (FMT == kKvInt4) {
+            cm[n][0] = fmaf(e0, vm[i][h], cm[n][0]);
+            cm[n][1] = fmaf(e1, vm[i][h], cm[n][1]);
+            e0 *= vs[i][h];
+            e1 *= vs[i][h];
+          }
+          pb[i][n][h] = transpose8(pack_bf16x2(e0, e1));
+        }
+    }
+    // ---- the second product
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+      if (FMT == kKvBf16) {
+#pragma unroll
+        for (int d = 0; d < KQ; ++d) {
+          uint32_t a[4];
+          ldsm4t(a, base + T::kV + T::chunk(i * 16 + ((lane >> 4) << 3) + (lane & 7), d * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int n = 0; n < NR; ++n) mma(o[d][n], a, pb[i][n][0], pb[i][n][1]);
+        }
+      } else {
+        // rows 2t, 2t + 1, 2t + 8, 2t + 9 of the 16: keys t, t + 4, t + 8, t + 12
+        constexpr int W = D / 64;   // words of a lane in a row: 2g, 2g + 1 (D = 128), or g
+        const uint32_t at = base + T::kV + (i * 16 + t) * T::kRow + g * (4 * W);
+        uint32_t x[4][W];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (W == 2)
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x[r][0]), "=r"(x[r][W - 1]) : "r"(at + r * 4 * T::kRow));
+          else
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[r][0]) : "r"(at + r * 4 * T::kRow));
+        }
+        // the same code of two rows side by side: codes 0..3 of a word, then 4..7
+        uint32_t lo[2][W], hi[2][W];
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            lo[k][w] = __byte_perm(x[2 * k][w], x[2 * k + 1][w], 0x5410);
+            hi[k][w] = __byte_perm(x[2 * k][w], x[2 * k + 1][w], 0x7632);
+          }
+#pragma unroll
+        for (int d = 0; d < KQ; ++d) {
+          const int c = 4 * (d & 3);
+          // D = 128: code d of word 2g and of word 2g + 1; D = 64: codes d and d + 4 of word g
+          const uint32_t y0 = D == 128 && d >= 4 ? hi[0][0] : lo[0][0], y2 = D == 128 && d >= 4 ? hi[1][0] : lo[1][0];
+          const uint32_t y1 = D == 128 && d < 4 ? lo[0][W - 1] : hi[0][W - 1], y3 = D == 128 && d < 4 ? lo[1][W - 1] : hi[1][W - 1];
+          const uint32_t a[4] = {code_pair8(y0 >> c), code_pair8(y1 >> c), code_pair8(y2 >> c), code_pair8(y3 >> c)};
+#pragma unroll
+          for (int n = 0; n < NR; ++n) mma(o[d][n], a, pb[i][n][0], pb[i][n][1]);
+        }
       }
     }
   }
-  // First d of accumulator pair i of this lane (o[i][0], o[i][1] in columns 2t, 2t + 1)
-  static __device__ __forceinline__ int d_of(int i, int e) {
-    const int t = threadIdx.x & 3;
-    if (FMT == kKvBf16) return i * 8 + 2 * t + e;
-    return 8 * (2 * t + e + 8 * (i >> 3)) + (i & 7);
+
+  // Sums over the lanes that hold other keys; the 4-bit minimum term joins the accumulators.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+          if (FMT == kKvInt4) cm[n][e] += __shfl_xor_sync(0xffffffffu, cm[n][e], x);
+        }
+        if (FMT == kKvInt4) {
+#pragma unroll
+          for (int i = 0; i < KQ; ++i) {
+            o[i][n][e] += cm[n][e];
+            o[i][n][2 + e] += cm[n][e];
+          }
+        }
+      }
   }
 };
 
@@ -407,26 +453,76 @@ __device__ __forceinline__ SeqTiles seq_tiles(const AttnParams& p, int b) {
   return s;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int NR>
 struct SplitCfg {
-  static constexpr int NT = 4;                                 // 8-key products of a step
-  static constexpr int KEYS = NT * 8;                          // keys of a warp's step
-  static constexpr int WARPS = FMT == kKvBf16 ? 4 : 8;
+  static constexpr bool BULK = FMT == kKvInt4;                 // bulk copies (else 16-byte asynchronous ones)
+  static constexpr int ROWS = NR * 8;                          // rows of a piece
+  static constexpr int KEYS = 32;                              // keys of a warp's step
+  static constexpr int WARPS = FMT == kKvBf16 ? 4 : (NR == 1 ? 8 : 12);
   static constexpr int STAGES = 3;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int TILE = KEYS * WARPS;                    // keys of a unit
   typedef Tile<D, FMT, KEYS> Layout;
   static constexpr int RING = WARPS * STAGES * Layout::kBytes;
-  static constexpr int MERGE = WARPS * kRowsMax * (D + 2) * 4; // the merge buffer reuses the ring
+  static constexpr int MERGE = WARPS * ROWS * (D + 2) * 4;     // the merge buffer reuses the ring
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE);
-  static constexpr int BLOCKS = 2 * (SMEM + 1024) <= 227 * 1024 ? 2 : 1;   // resident blocks of an SM
+  // resident blocks of an SM
+  static constexpr int BLOCKS = 2 * (SMEM + 1536) <= 227 * 1024 && (FMT == kKvBf16 || NR == 1) ? 2 : 1;
 };
 
-// Copies of one warp step: lane l resolves key l's page, the lanes then copy the
+// Bulk copies of warp steps of 4-bit pages. A step is up to KEYS / 16 runs of
+// neighbouring rows (a run: the part of one page inside it), each four copies:
+// keys, values and their scale pairs. Lane 4 r + w issues copy w of run r; the page
+// of the next step is looked up while the present one's copies are issued.
+template <int D, int KEYS>
+struct BulkLanes {
+  typedef Tile<D, kKvInt4, KEYS> T;
+  const uint8_t* base;
+  long long page_stride;
+  int row_bytes, dst, run, offset;   // offset: first key of this lane's run in the step
+  bool active;
+
+  __device__ __forceinline__ void init(const KvParams& kv) {
+    const int lane = threadIdx.x & 31, which = lane & 3;
+    run = min(1 << kv.page_shift, KEYS);
+    offset = (lane >> 2) * run;
+    active = offset < KEYS;
+    const bool scales = which >= 2;
+    base = which == 0 ? kv.k : which == 1 ? kv.v
+                             : reinterpret_cast<const uint8_t*>(which == 2 ? kv.k_scale : kv.v_scale);
+    page_stride = scales ? kv.scale_stride * 4 : kv.page_stride;
+    row_bytes = scales ? 4 : T::kRow;
+    dst = (which == 0 ? 0 : which == 1 ? T::kV : which == 2 ? T::kKs : T::kVs) + offset * row_bytes;
+  }
+  // page of this lane's run of the step at `key`, -1 when nobody sees it
+  __device__ __forceinline__ int page(const KvParams& kv, int b, int key, const Sight& sight) const {
+    const int k = key + offset;
+    return active && k < sight.len && (k + run > sight.lo || k < sight.sinks) ? kv_page(kv, b, k) : -1;
+  }
+  __device__ __forceinline__ void issue(const KvParams& kv, int head, int key, int page, uint32_t stage, uint64_t* bar) const {
+    const int lane = threadIdx.x & 31;
+    const uint32_t runs = __popc(__ballot_sync(0xffffffffu, page >= 0)) >> 2;
+    if (lane == 0) {
+      if (runs) mbar_arrive_expect_tx(bar, runs * run * (2 * T::kRow + 8));
+      else mbar_arrive(bar);
+    }
+    __syncwarp();
+    if (page >= 0)
+      bulk_load_at(stage + dst, base + page * page_stride + static_cast<long long>(kv_row_in_page(kv, head, key + offset)) * row_bytes,
+                   run * row_bytes, bar);
+  }
+  static __device__ __forceinline__ void bulk_load_at(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+  }
+};
+
+// Copies of one warp step of bf16 pages: lane l resolves key l's page, the lanes then copy the
 // rows chunk by chunk. Keys that no row sees become zeros.
-template <int D, int FMT, int KEYS>
+template <int D, int KEYS>
 __device__ __forceinline__ void load_step(const AttnParams& p, int b, int head, int key, const Sight& sight, uint32_t dst) {
-  typedef Tile<D, FMT, KEYS> T;
+  typedef Tile<D, kKvBf16, KEYS> T;
   static_assert(KEYS == 32, "one lane per key");
   const int lane = threadIdx.x & 31;
   int page = -1, row = 0;
@@ -442,14 +538,8 @@ __device__ __forceinline__ void load_step(const AttnParams& p, int b, int head, 
     const long long o = __shfl_sync(0xffffffffu, off, r);
     const int n = o >= 0 ? 16 : 0;
     const long long a = o >= 0 ? o + c * 16 : 0;
-    cp16(dst + T::k_chunk(r, c), p.kv.k + a, n);
-    cp16(dst + T::v_chunk(r, c), p.kv.v + a, n);
-  }
-  if (FMT == kKvInt4) {
-    const long long a = page >= 0 ? page * p.kv.scale_stride + row : 0;
-    const int n = page >= 0 ? 4 : 0;
-    cp4(dst + T::kKs + lane * 4, p.kv.k_scale + a, n);
-    cp4(dst + T::kVs + lane * 4, p.kv.v_scale + a, n);
+    cp16(dst + T::chunk(r, c), p.kv.k + a, n);
+    cp16(dst + T::kV + T::chunk(r, c), p.kv.v + a, n);
   }
 }
 
@@ -475,15 +565,23 @@ __device__ __forceinline__ void store_row_part(const AttnParams& p, int first, i
     p.lse[static_cast<long long>(hq) * p.kv.M + token] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(SplitCfg<D, FMT>::THREADS, SplitCfg<D, FMT>::BLOCKS)
+template <int D, int FMT, int NR>
+__global__ void __launch_bounds__(SplitCfg<D, FMT, NR>::THREADS, SplitCfg<D, FMT, NR>::BLOCKS)
     k8_attend_split(const __grid_constant__ AttnParams p) {
-  typedef SplitCfg<D, FMT> C;
+  typedef SplitCfg<D, FMT, NR> C;
   typedef typename C::Layout L;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int scan[C::WARPS];
-  __shared__ int found[4];   // sequence, units before it, ...
+  __shared__ int found[3];   // sequence of the first unit, tiles before it; whether this block arrived last
+  __shared__ uint64_t full[C::WARPS][C::STAGES];
+  __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (C::BULK) {
+    if (lane < C::STAGES) mbar_init(&full[warp][lane], 1);
+    if (threadIdx.x == 0) abort_flag = 0;
+    fence_mbar_init();
+    __syncwarp();   // (the block's barriers below order the flag)
+  }
   pdl_wait();
 
   // ---- deal the units: prefix sums over the sequences' tiles
@@ -541,7 +639,10 @@ __global__ void __launch_bounds__(SplitCfg<D, FMT>::THREADS, SplitCfg<D, FMT>::B
   }
 
   const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * L::kBytes);
-  Rows16<D, FMT, C::NT> r16;
+  RowState<D, FMT, NR, C::KEYS> state;
+  BulkLanes<D, C::KEYS> bulk;
+  if (C::BULK) bulk.init(p.kv);
+  uint32_t issued = 0, used = 0;   // steps of this warp so far (bulk form): slot and parity of each
   SeqTiles st = seq_tiles<C::TILE>(p, b);
   for (long long u = u0; u < u1;) {
     while (u >= before + static_cast<long long>(st.tiles) * Hkv) {
@@ -564,89 +665,122 @@ __global__ void __launch_bounds__(SplitCfg<D, FMT>::THREADS, SplitCfg<D, FMT>::B
     auto key_of = [&](int i) {
       return (i < st.sink_tiles ? i : st.lo_tile + i - st.sink_tiles) * C::TILE + warp * C::KEYS;
     };
+    int page = -1;   // bulk form: this lane's page of the next step to copy
+    auto issue = [&](int i) {
+      const uint32_t slot = issued % C::STAGES;
+      bulk.issue(p.kv, head, key_of(i), page, ring + slot * L::kBytes, &full[warp][slot]);
+      ++issued;
+      page = i + 1 < t1 ? bulk.page(p.kv, b, key_of(i + 1), sight) : -1;
+    };
+    if (C::BULK) {
+      page = bulk.page(p.kv, b, key_of(t0), sight);
+      for (int i = t0; i < min(t0 + C::STAGES, t1); ++i) issue(i);
+    } else {
 #pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) {
-      if (t0 + i < t1) load_step<D, FMT, C::KEYS>(p, b, head, key_of(t0 + i), sight, ring + i * L::kBytes);
-      cp_commit();
+      for (int i = 0; i < C::STAGES - 1; ++i) {
+        if (t0 + i < t1) load_step<D, C::KEYS>(p, b, head, key_of(t0 + i), sight, ring + i * L::kBytes);
+        cp_commit();
+      }
     }
     {
-      const int g = lane >> 2, a0 = min(g, sight.rows - 1), a1 = min(g + 8, sight.rows - 1);
-      r16.load_q(g < sight.rows ? p.q + q_row(p, st.first, head, a0) * D : nullptr,
-                 g + 8 < sight.rows ? p.q + q_row(p, st.first, head, a1) * D : nullptr);
-      r16.p0 = st.pos0 + a0 / p.group;
-      r16.p1 = st.pos0 + a1 / p.group;
-      r16.reset();
+      const bf16* r[NR];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const int row = n * 8 + (lane >> 2);
+        r[n] = row < sight.rows ? p.q + q_row(p, st.first, head, row) * D : nullptr;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          state.pos[n][e] = st.pos0 + min(n * 8 + 2 * (lane & 3) + e, sight.rows - 1) / p.group;
+      }
+      state.load(r);
     }
     int slot = 0;
+    bool ok = true;
     for (int i = t0; i < t1; ++i) {
-      const int nx = i + C::STAGES - 1;
-      const int ns = slot == 0 ? C::STAGES - 1 : slot - 1;
-      if (nx < t1) load_step<D, FMT, C::KEYS>(p, b, head, key_of(nx), sight, ring + ns * L::kBytes);
-      cp_commit();
-      cp_wait<C::STAGES - 1>();
-      __syncwarp();
       const int key = key_of(i);
       // a step none of whose keys is seen is skipped (behind the end, between sinks and window)
-      if (key < st.len && (key + C::KEYS > st.lo || key < p.sinks))
-        r16.template step<C::KEYS>(ring + slot * L::kBytes, 0, key, sight, p.scale_log2);
-      __syncwarp();
-      slot = slot == C::STAGES - 1 ? 0 : slot + 1;
+      const bool any = key < st.len && (key + C::KEYS > st.lo || key < p.sinks);
+      if (C::BULK) {
+        const uint32_t at = used % C::STAGES;
+        ok = warp_wait(&full[warp][at], (used / C::STAGES) & 1, &abort_flag, p.kv.status, kStatusWaitFull, p.wait_ns);
+        if (!ok) break;
+        ++used;
+        if (any) state.step(ring + at * L::kBytes, key, sight, p.scale_log2);
+        __syncwarp();   // every lane has read the slot
+        if (i + C::STAGES < t1) issue(i + C::STAGES);
+      } else {
+        const int nx = i + C::STAGES - 1;
+        const int ns = slot == 0 ? C::STAGES - 1 : slot - 1;
+        if (nx < t1) load_step<D, C::KEYS>(p, b, head, key_of(nx), sight, ring + ns * L::kBytes);
+        cp_commit();
+        cp_wait<C::STAGES - 1>();
+        __syncwarp();
+        if (any) state.step(ring + slot * L::kBytes, key, sight, p.scale_log2);
+        __syncwarp();
+        slot = slot == C::STAGES - 1 ? 0 : slot + 1;
+      }
     }
-    cp_wait<0>();
+    if (C::BULK) {
+      if (!ok)   // this warp's copies in flight land before the ring is used for anything else
+        for (; used != issued; ++used) drain_wait(&full[warp][used % C::STAGES], (used / C::STAGES) & 1);
+    } else {
+      cp_wait<0>();
+    }
     // ---- the warps' rows together
-    r16.finish();
+    state.finish();
     __syncthreads();
-    float* mo = reinterpret_cast<float*>(smem);                      // [warp][16][D]
-    float* mm = mo + C::WARPS * kRowsMax * D;                        // [warp][16] maximum, then sum
-    float* ml = mm + C::WARPS * kRowsMax;
-    {
-      const int g = lane >> 2;
-      float* w0 = mo + (warp * kRowsMax + g) * D;
-      float* w1 = w0 + 8 * D;
+    if (C::BULK && abort_flag) return;   // every copy has landed; check() reports the status
+    float* mo = reinterpret_cast<float*>(smem);                      // [warp][row][D]
+    float* mm = mo + C::WARPS * C::ROWS * D;                        // [warp][row] maximum, then sum
+    float* ml = mm + C::WARPS * C::ROWS;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int d = r16.d_of(i, e);
-          w0[d] = r16.o[i][e];
-          w1[d] = r16.o[i][2 + e];
+      for (int e = 0; e < 2; ++e) {
+        const int row = n * 8 + 2 * (lane & 3) + e;
+        float* w = mo + (warp * C::ROWS + row) * D;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          w[state.d_of(i, 0)] = state.o[i][n][e];
+          w[state.d_of(i, 1)] = state.o[i][n][2 + e];
+        }
+        if (lane < 4) {
+          mm[warp * C::ROWS + row] = state.m[n][e];
+          ml[warp * C::ROWS + row] = state.l[n][e];
         }
       }
-      if ((lane & 3) == 0) {
-        mm[warp * kRowsMax + g] = r16.m0;
-        mm[warp * kRowsMax + g + 8] = r16.m1;
-        ml[warp * kRowsMax + g] = r16.l0;
-        ml[warp * kRowsMax + g + 8] = r16.l1;
-      }
-    }
     __syncthreads();
-    constexpr int PER = kRowsMax * D / C::THREADS;   // values of a thread, in one row
-    const int row = threadIdx.x * PER / D, d0 = threadIdx.x * PER % D;
+    constexpr int PER = C::THREADS * 4 >= C::ROWS * D ? 4 : C::THREADS * 8 >= C::ROWS * D ? 8 : 16;
+    static_assert(PER * C::THREADS >= C::ROWS * D && D % PER == 0, "values of a thread: 4, 8 or 16 of one row");
+    const bool works = static_cast<int>(threadIdx.x) * PER < C::ROWS * D;
+    const int row = works ? threadIdx.x * PER / D : 0, d0 = threadIdx.x * PER % D;
     float acc[PER], top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, mm[w * kRowsMax + row]);
+    for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, mm[w * C::ROWS + row]);
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
 #pragma unroll
     for (int w = 0; w < C::WARPS; ++w) {
-      const float f = top == -INFINITY ? 0.f : ex2(mm[w * kRowsMax + row] - top);
-      sum += f * ml[w * kRowsMax + row];
+      const float f = top == -INFINITY ? 0.f : ex2(mm[w * C::ROWS + row] - top);
+      sum += f * ml[w * C::ROWS + row];
 #pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, mo[(w * kRowsMax + row) * D + d0 + e], acc[e]);
+      for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, mo[(w * C::ROWS + row) * D + d0 + e], acc[e]);
     }
     const bool whole = t0 == 0 && t1 == st.tiles;
     if (whole) {
-      if (row < sight.rows) store_row_part<D, PER>(p, st.first, head, row, d0, acc, top, sum);
+      if (works && row < sight.rows) store_row_part<D, PER>(p, st.first, head, row, d0, acc, top, sum);
     } else {
       // partial sums: slot 2i + 1 for a head that begins in this block, 2i for one begun before
       const int c0 = unit_owner(s0, G, U), c1 = unit_owner(s1 - 1, G, U);
       float* mine = p.part + static_cast<long long>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * kPartFloats;
+      if (works) {
 #pragma unroll
-      for (int e = 0; e < PER; e += 4)
-        __stcg(reinterpret_cast<float4*>(mine + row * D + d0 + e), make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]));
-      if (d0 == 0) {
-        __stcg(mine + kRowsMax * D + row, top);
-        __stcg(mine + kRowsMax * D + kRowsMax + row, sum);
+        for (int e = 0; e < PER; e += 4)
+          __stcg(reinterpret_cast<float4*>(mine + row * D + d0 + e), make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]));
+      }
+      if (works && d0 == 0) {
+        __stcg(mine + C::ROWS * D + row, top);
+        __stcg(mine + C::ROWS * D + C::ROWS + row, sum);
       }
       __threadfence();
       __syncthreads();
@@ -656,14 +790,14 @@ __global__ void __launch_bounds__(SplitCfg<D, FMT>::THREADS, SplitCfg<D, FMT>::B
         __threadfence();
         top = -INFINITY;
         for (int c = c0; c <= c1; ++c)
-          top = fmaxf(top, __ldcg(p.part + static_cast<long long>(2 * c + (c == c0)) * kPartFloats + kRowsMax * D + row));
+          top = fmaxf(top, __ldcg(p.part + static_cast<long long>(2 * c + (c == c0)) * kPartFloats + C::ROWS * D + row));
         sum = 0.f;
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] = 0.f;
         for (int c = c0; c <= c1; ++c) {
           const float* s = p.part + static_cast<long long>(2 * c + (c == c0)) * kPartFloats;
-          const float f = top == -INFINITY ? 0.f : ex2(__ldcg(s + kRowsMax * D + row) - top);
-          sum += f * __ldcg(s + kRowsMax * D + kRowsMax + row);
+          const float f = top == -INFINITY ? 0.f : ex2(__ldcg(s + C::ROWS * D + row) - top);
+          sum += f * __ldcg(s + C::ROWS * D + C::ROWS + row);
 #pragma unroll
           for (int e = 0; e < PER; e += 4) {
             const float4 x = __ldcg(reinterpret_cast<const float4*>(s + row * D + d0 + e));
@@ -673,151 +807,14 @@ __global__ void __launch_bounds__(SplitCfg<D, FMT>::THREADS, SplitCfg<D, FMT>::B
             acc[e + 3] = fmaf(f, x.w, acc[e + 3]);
           }
         }
-        if (row < sight.rows) store_row_part<D, PER>(p, st.first, head, row, d0, acc, top, sum);
+        if (works && row < sight.rows) store_row_part<D, PER>(p, st.first, head, row, d0, acc, top, sum);
         if (threadIdx.x == 0) p.counters[c0] = 0;
       }
     }
+    if (C::BULK) fence_proxy_async_smem();   // the merge buffer's stores come before the next bulk copies
     __syncthreads();   // the merge buffer is the ring again
     u = before + static_cast<long long>(head) * st.tiles + t1;
   }
-}
-
-// ---------------------------------------------------------------- rows form
-template <int D, int FMT>
-struct RowsCfg {
-  static constexpr int WARPS = 8;
-  static constexpr int THREADS = WARPS * 32;
-  static constexpr int ROWS = WARPS * 16;
-  static constexpr int NT = 4;
-  static constexpr int TILE = 64;          // keys of a block tile
-  static constexpr int STAGES = 2;
-  typedef Tile<D, FMT, TILE> Layout;
-  static constexpr int SMEM = STAGES * Layout::kBytes;
-};
-
-template <int D, int FMT>
-__global__ void __launch_bounds__(RowsCfg<D, FMT>::THREADS, 1) k8_attend_rows(const __grid_constant__ AttnParams p) {
-  typedef RowsCfg<D, FMT> C;
-  typedef typename C::Layout L;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  const int b = blockIdx.z, head = blockIdx.y;
-  const KvSeq q = kv_seq(p.kv, b);
-  const int rows = q.n * p.group;
-  // the longest (last) row tiles first
-  const int tile = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);
-  const int r0 = tile * C::ROWS;
-  if (r0 >= rows) return;
-  const int r1 = min(r0 + C::ROWS, rows);
-  Sight sight;
-  sight.pos0 = q.len - q.n + r0 / p.group;
-  sight.last = q.len - q.n + (r1 - 1) / p.group;
-  sight.rows = rows;
-  sight.group = p.group;
-  sight.len = min(q.len, sight.last + 1);
-  sight.window = p.window;
-  sight.sinks = p.sinks;
-  sight.lo = p.window > 0 ? max(0, sight.pos0 - p.window + 1) : 0;
-  const int lo_tile = sight.lo / C::TILE;
-  const int sink_tiles = min((min(p.sinks, max(sight.len, 0)) + C::TILE - 1) / C::TILE, lo_tile);
-  const int tiles = sight.len > 0 ? sink_tiles + (sight.len + C::TILE - 1) / C::TILE - lo_tile : 0;
-  auto key_of = [&](int i) { return (i < sink_tiles ? i : lo_tile + i - sink_tiles) * C::TILE; };
-
-  Rows16<D, FMT, C::NT> r16;
-  const int g = lane >> 2;
-  const int a0 = r0 + warp * 16 + g, a1 = a0 + 8;
-  r16.load_q(a0 < rows ? p.q + q_row(p, q.first, head, a0) * D : nullptr,
-             a1 < rows ? p.q + q_row(p, q.first, head, a1) * D : nullptr);
-  r16.p0 = q.len - q.n + min(a0, rows - 1) / p.group;
-  r16.p1 = q.len - q.n + min(a1, rows - 1) / p.group;
-  r16.reset();
-  // a warp's own range of positions, for its masks
-  Sight mine = sight;
-  mine.pos0 = q.len - q.n + min(r0 + warp * 16, rows - 1) / p.group;
-  mine.last = q.len - q.n + min(r0 + warp * 16 + 15, rows - 1) / p.group;
-  const bool live = r0 + warp * 16 < rows;
-
-  // copies of one block tile: 8 warps take 8 keys each
-  auto load = [&](int i, int stage) {
-    const uint32_t dst = smem_u32(smem) + stage * L::kBytes;
-    const int key0 = key_of(i);
-    constexpr int PER = C::TILE / C::WARPS;   // keys of a warp
-    int page = -1, row = 0;
-    if (lane < PER && sight.any(key0 + warp * PER + lane)) {
-      page = kv_page(p.kv, b, key0 + warp * PER + lane);
-      row = kv_row_in_page(p.kv, head, key0 + warp * PER + lane);
-    }
-    const long long off = page >= 0 ? page * p.kv.page_stride + static_cast<long long>(row) * (L::kChunks * 16) : -1;
-    constexpr int INSTR = (PER * L::kChunks + 31) / 32;
-#pragma unroll
-    for (int k = 0; k < INSTR; ++k) {
-      const int at = k * 32 + lane, r = at / L::kChunks, c = at % L::kChunks;
-      const long long o = __shfl_sync(0xffffffffu, off, r < PER ? r : 0);
-      if (r < PER) {
-        const int n = o >= 0 ? 16 : 0;
-        const long long a = o >= 0 ? o + c * 16 : 0;
-        cp16(dst + L::k_chunk(warp * PER + r, c), p.kv.k + a, n);
-        cp16(dst + L::v_chunk(warp * PER + r, c), p.kv.v + a, n);
-      }
-    }
-    if (FMT == kKvInt4 && lane < PER) {
-      const long long a = page >= 0 ? page * p.kv.scale_stride + row : 0;
-      const int n = page >= 0 ? 4 : 0;
-      cp4(dst + L::kKs + (warp * PER + lane) * 4, p.kv.k_scale + a, n);
-      cp4(dst + L::kVs + (warp * PER + lane) * 4, p.kv.v_scale + a, n);
-    }
-  };
-
-  if (tiles > 0) load(0, 0);
-  cp_commit();
-  for (int i = 0; i < tiles; ++i) {
-    if (i + 1 < tiles) load(i + 1, (i + 1) & 1);
-    cp_commit();
-    cp_wait<1>();
-    __syncthreads();
-    if (live) {
-      const int key0 = key_of(i);
-#pragma unroll 1
-      for (int k = 0; k < C::TILE; k += C::NT * 8) {
-        const int key = key0 + k;
-        // skip what none of this warp's rows sees
-        if (key > mine.last || (mine.window > 0 && key + C::NT * 8 <= mine.pos0 - mine.window + 1 && key >= mine.sinks))
-          continue;
-        r16.template step<C::TILE>(smem_u32(smem) + (i & 1) * L::kBytes, k, key, mine, p.scale_log2);
-      }
-    }
-    __syncthreads();
-  }
-  cp_wait<0>();
-  r16.finish();
-  // ---- rows out
-  auto put = [&](int r, int h, float top, float sum) {
-    if (r >= rows) return;
-    const int token = q.first + r / p.group, hq = head * p.group + r % p.group;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    bf16* dst = p.out + (static_cast<long long>(token) * p.Hq + hq) * D;
-    if (FMT == kKvBf16) {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<uint32_t*>(dst + r16.d_of(i, 0)) = pack_bf16x2(r16.o[i][2 * h] * inv, r16.o[i][2 * h + 1] * inv);
-    } else {   // a lane holds whole runs of 8 d
-#pragma unroll
-      for (int w = 0; w < D / 64; ++w) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float f[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = r16.o[w * 8 + i][2 * h + e] * inv;
-          *reinterpret_cast<uint4*>(dst + r16.d_of(w * 8, e)) = pack8(f);
-        }
-      }
-    }
-    if ((lane & 3) == 0 && p.lse)
-      p.lse[static_cast<long long>(hq) * p.kv.M + token] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
-  };
-  put(a0, 0, r16.m0, r16.l0);
-  put(a1, 1, r16.m1, r16.l1);
 }
 
 }  // namespace k8

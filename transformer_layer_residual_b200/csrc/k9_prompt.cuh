@@ -110,16 +110,8 @@ struct Ctrl {
   int abort_flag;
 };
 
-// The wait that an aborting role ends with: bounded, sets nothing.
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity))
-    if (globaltimer() - t0 > FNL_WAIT_NS) return;
-}
-
 struct Params {
   AttnParams a;
-  unsigned long long wait_ns;
   int stall;   // fault injection for the status-path tests: block 0 withholds its first key tile
 };
 
@@ -208,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * bp * 128;
       const int row = kv_row_in_page(p.kv, head, key);
       for (int kv = 0; kv < 2; ++kv) {
-        ok = warp_wait(&ctrl->empty[slot], ph ^ 1u, abortf, status, kStatusWaitEmpty, prm.wait_ns);
+        ok = warp_wait(&ctrl->empty[slot], ph ^ 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
         if (!ok) break;
         if (withhold) {
           withhold = false;
@@ -273,8 +265,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) umma_commit(bar);
       __syncwarp();
     };
-    bool ok = n == 0 || (warp_wait(&ctrl->q_full, 0, abortf, status, kStatusWaitConv, prm.wait_ns) &&
-                         warp_wait(&ctrl->full[slot], ph, abortf, status, kStatusWaitFull, prm.wait_ns));
+    bool ok = n == 0 || (warp_wait(&ctrl->q_full, 0, abortf, status, kStatusWaitConv, p.wait_ns) &&
+                         warp_wait(&ctrl->full[slot], ph, abortf, status, kStatusWaitFull, p.wait_ns));
     if (ok && n > 0) {
       tc_fence_after();
       if (n0 > 0) qk(0, slot);
@@ -285,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < n && ok; ++i) {
       // V of tile i at `slot`, K of tile i + 1 behind it
       const int vs = slot;
-      ok = warp_wait(&ctrl->full[slot], ph, abortf, status, kStatusWaitFull, prm.wait_ns);
+      ok = warp_wait(&ctrl->full[slot], ph, abortf, status, kStatusWaitFull, p.wait_ns);
       if (!ok) break;
       const int key = key_of(i);
       if (key + TILE > sight.len || (key < sight.lo && key + TILE > sight.sinks)) {
@@ -304,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int s = 0; s < 2 && ok; ++s) {
         const int ns = s ? n1 : n0;
         if (i < ns) {
-          ok = warp_wait(&ctrl->p_full[s], i & 1, abortf, status, kStatusWaitConv, prm.wait_ns);
+          ok = warp_wait(&ctrl->p_full[s], i & 1, abortf, status, kStatusWaitConv, p.wait_ns);
           if (!ok) break;
           tc_fence_after();
           pv(s, vs, i == 0);
@@ -313,7 +305,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (s == 1) commit(&ctrl->empty[vs]);
         if (i + 1 < ns) {
           if (!have_k) {
-            ok = warp_wait(&ctrl->full[ks], ph, abortf, status, kStatusWaitFull, prm.wait_ns);
+            ok = warp_wait(&ctrl->full[ks], ph, abortf, status, kStatusWaitFull, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
             have_k = true;
@@ -328,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (!ok || *abortf) {   // every product issued is done before TMEM is freed
       commit(&ctrl->drain);
-      if (lane == 0) drain_wait(&ctrl->drain, 0);
+      if (lane == 0) k8::drain_wait(&ctrl->drain, 0);
       __syncwarp();
     }
   } else if (warp < 4) {
@@ -367,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     f32x2 sum2 = pk2(0.f, 0.f);
     bool ok = true;
     for (int i = 0; i < ns; ++i) {
-      ok = warp_wait(&ctrl->s_full[s], i & 1, abortf, status, kStatusWaitTmemFull, prm.wait_ns);
+      ok = warp_wait(&ctrl->s_full[s], i & 1, abortf, status, kStatusWaitTmemFull, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
       uint32_t x[TILE];
@@ -431,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     unpk2(sum2, a, c);
     const float sum = a + c;
     if (ok && ns > 0) {
-      ok = warp_wait(&ctrl->o_full[s], 0, abortf, status, kStatusWaitTmemFull, prm.wait_ns);
+      ok = warp_wait(&ctrl->o_full[s], 0, abortf, status, kStatusWaitTmemFull, p.wait_ns);
       tc_fence_after();
     }
     if (ok) {
@@ -469,7 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (warp == 0 && *abortf)   // after an abort nobody has waited for the copies in flight
     for (int s = 0; s < C::STAGES; ++s)
-      if (ctrl->armed & (1u << s)) drain_wait(&ctrl->full[s], (ctrl->armed_parity >> s) & 1);
+      if (ctrl->armed & (1u << s)) k8::drain_wait(&ctrl->full[s], (ctrl->armed_parity >> s) & 1);
 }
 
 }  // namespace k9
