@@ -97,7 +97,7 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
 
 def test_null_handle_is_refused():
     L = fnl.lib()
-    c, b = fnl._KvCache(), fnl._KvBatch()
+    c, b = ctypes.byref(fnl._KvCache()), ctypes.byref(fnl._KvBatch())
     assert L.fnl_rope_append_kv(None, None, c, b, 1, 1, None, None, None, None, None, 0, 0, 0, None) == 1
     assert L.fnl_kv_gather(None, None, c, b, 1, None, None) == 1
     assert L.fnl_paged_attention(None, None, c, b, 1, 1, None, ctypes.c_float(1), 0, 0, None, None) == 1

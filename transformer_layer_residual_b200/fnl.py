@@ -93,10 +93,10 @@ def lib() -> ctypes.CDLL:
     L.fnl_add_bias_norm_gelu_fp8.argtypes = [P, P, P, P, P, P, P, P, I, F, P, P, P, I, I, I, P, P, P]
     L.fnl_add_norm_qkv_static.argtypes = [P, P, P, P, P, P, I, F, P, P, I, I, I, I, I, P, P, P, P, P]
     L.fnl_check_static.argtypes = [P]
-    KC, KB = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch)
-    L.fnl_rope_append_kv.argtypes = [P, P, KC, KB, I, I, P, P, P, P, P, I, I, I, P]
-    L.fnl_kv_gather.argtypes = [P, P, KC, KB, I, P, P]
-    L.fnl_paged_attention.argtypes = [P, P, KC, KB, I, I, P, F, I, I, P, P]
+    # the cache and the batch go as the addresses of their structures
+    L.fnl_rope_append_kv.argtypes = [P, P, P, P, I, I, P, P, P, P, P, I, I, I, P]
+    L.fnl_kv_gather.argtypes = [P, P, P, P, I, P, P]
+    L.fnl_paged_attention.argtypes = [P, P, P, P, I, I, P, F, I, I, P, P]
     for name in EXPORTED:
         if getattr(L, name).restype is None and name not in ("fnl_status_string", "fnl_last_error", "fnl_last_plan"):
             getattr(L, name).restype = I
@@ -441,9 +441,12 @@ class KVCache:
                 raise ValueError("k_scale and v_scale must have the same page stride")
         elif k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 cache has no k_scale and v_scale")
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
+        if any(t is not None and t.get_device() != self.index for t in (v, k_scale, v_scale)):
+            raise ValueError("the cache's tensors must be on one device")
         self.c = _KvCache(KV_FORMATS[self.format], n, self.page_size, self.Hkv, self.D, _p(k), _p(v), _p(k_scale),
                           _p(v_scale), stride, scale_stride)
+        self.ptr = ctypes.addressof(self.c)
 
     @staticmethod
     def _pages(t, name, shape, dtype):
@@ -488,23 +491,26 @@ class KVBatch:
         if block_table.dim() != 2 or block_table.shape[0] != B:
             raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
         self.cu_q, self.kv_len, self.block_table, self.max_q = cu_q, kv_len, block_table, int(max_q)
-        self.device = kv_len.device
+        self.device, self.index = kv_len.device, kv_len.get_device()
         if cu_q.device != self.device or block_table.device != self.device:
             raise ValueError("cu_q, kv_len and block_table must be on one device")
         self.c = _KvBatch(B, self.max_q, _p(cu_q), _p(kv_len), _p(block_table), block_table.shape[1])
+        self.ptr = ctypes.addressof(self.c)
 
 
 def _kv_stream(h, cache, batch, stream):
     """The call's stream: `stream`, or the current one of the handle's device."""
-    if cache.device.index != h.device or batch.device.index != h.device:
+    if cache.index != h.device or batch.index != h.device:
         raise ValueError(f"the cache and the batch must be on the handle's device, cuda:{h.device}")
-    return ctypes.c_void_p((torch.cuda.current_stream(h.device) if stream is None else stream).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(h.device) if stream is None else stream.cuda_stream
 
 
 def _kv_need(h, t, name, shape, dtype=torch.bfloat16):
+    """The data pointer of t after its checks (a decode step makes these calls once a layer: the one test first)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == h.device and t.is_contiguous():
+        return t.data_ptr()
     _need(t, name, shape, dtype)
-    if t is not None and t.device.index != h.device:
-        raise ValueError(f"{name} must be on the handle's device, cuda:{h.device}")
+    raise ValueError(f"{name} must be on the handle's device, cuda:{h.device}")
 
 
 def rope_append_kv(h: Handle, cache: KVCache, batch: KVBatch, q, k, v, cos=None, sin=None, interleaved=False,
@@ -513,27 +519,32 @@ def rope_append_kv(h: Handle, cache: KVCache, batch: KVBatch, q, k, v, cos=None,
     them), cos and sin fp32 [max_pos, rot_dim / 2]. k (rotated) and v go to their
     pages; q_out (allocated when not given; may be q) gets the rotated q. Without
     cos and sin nothing is rotated and q is returned as it is. Returns dict(q)."""
-    Hkv, D = cache.Hkv, cache.D
-    M = k.shape[1]
-    _kv_need(h, k, "k", (Hkv, M, D))
-    _kv_need(h, v, "v", (Hkv, M, D))
+    if k.dim() != 3:
+        raise ValueError("k must be [Hkv, M, D]")
+    Hkv, M, D = cache.Hkv, k.shape[1], cache.D
+    kp = _kv_need(h, k, "k", (Hkv, M, D))
+    vp = _kv_need(h, v, "v", (Hkv, M, D))
     s = _kv_stream(h, cache, batch, stream)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin are given together")
     if cos is None:
         if q_out is not None:
             raise ValueError("q_out is written by the rotation only: give cos and sin")
-        st = lib().fnl_rope_append_kv(h.ptr, s, cache.c, batch.c, M, 0, None, _p(k), _p(v), None, None, 0, 0, 0, None)
+        st = lib().fnl_rope_append_kv(h.ptr, s, cache.ptr, batch.ptr, M, 0, None, kp, vp, None, None, 0, 0, 0, None)
     else:
-        _kv_need(h, q, "q", (q.shape[0], M, D))
-        if cos.dim() != 2:
-            raise ValueError("cos and sin must be [max_pos, rot_dim / 2]")
-        _kv_need(h, cos, "cos", cos.shape, torch.float32)
-        _kv_need(h, sin, "sin", cos.shape, torch.float32)
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        _kv_need(h, q_out, "q_out", q.shape)
-        st = lib().fnl_rope_append_kv(h.ptr, s, cache.c, batch.c, M, q.shape[0], _p(q), _p(k), _p(v), _p(cos), _p(sin),
-                                      2 * cos.shape[1], cos.shape[0], int(bool(interleaved)), _p(q_out))
+        if q.dim() != 3 or cos.dim() != 2:
+            raise ValueError("q must be [Hq, M, D], cos and sin [max_pos, rot_dim / 2]")
+        shape, table = (q.shape[0], M, D), cos.shape
+        qp = _kv_need(h, q, "q", shape)
+        cp = _kv_need(h, cos, "cos", table, torch.float32)
+        sp = _kv_need(h, sin, "sin", table, torch.float32)
+        if q_out is None:
+            q_out = torch.empty_like(q)
+            op = q_out.data_ptr()
+        else:
+            op = _kv_need(h, q_out, "q_out", shape)
+        st = lib().fnl_rope_append_kv(h.ptr, s, cache.ptr, batch.ptr, M, shape[0], qp, kp, vp, cp, sp, 2 * table[1],
+                                      table[0], 1 if interleaved else 0, op)
     if st != FNL_OK:
         h._raise(st, "fnl_rope_append_kv")
     return {"q": q if cos is None else q_out}
@@ -541,8 +552,8 @@ def rope_append_kv(h: Handle, cache: KVCache, batch: KVBatch, q, k, v, cos=None,
 
 def kv_gather(h: Handle, cache: KVCache, batch: KVBatch, M=None, k=None, v=None, stream=None):
     """fnl_kv_gather: the batch's new tokens read back from their pages, k and v
-    bf16 [Hkv, M, D]. M (the packed rows) comes from k, or is given, or, when
-    neither is, read from cu_q, which waits for the device. Returns dict(k, v)."""
+    bf16 [Hkv, M, D]. M (the packed rows) comes from k or v, or is given, or, when
+    none is, read from cu_q, which waits for the device. Returns dict(k, v)."""
     if k is not None or v is not None:
         M = (v if k is None else k).shape[1]
     elif M is None:
@@ -551,9 +562,7 @@ def kv_gather(h: Handle, cache: KVCache, batch: KVBatch, M=None, k=None, v=None,
     s = _kv_stream(h, cache, batch, stream)
     k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
     v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
-    _kv_need(h, k, "k", shape)
-    _kv_need(h, v, "v", shape)
-    st = lib().fnl_kv_gather(h.ptr, s, cache.c, batch.c, M, _p(k), _p(v))
+    st = lib().fnl_kv_gather(h.ptr, s, cache.ptr, batch.ptr, M, _kv_need(h, k, "k", shape), _kv_need(h, v, "v", shape))
     if st != FNL_OK:
         h._raise(st, "fnl_kv_gather")
     return {"k": k, "v": v}
@@ -565,14 +574,19 @@ def paged_attention(h: Handle, cache: KVCache, batch: KVBatch, q, scale=None, wi
     window and `sinks` first tokens that stay visible when window > 0. scale
     defaults to D ** -0.5; lse (fp32 [Hq, M]) is filled when given. Returns
     dict(out, lse)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [Hq, M, D]")
     Hq, M, D = q.shape
-    _kv_need(h, q, "q", (Hq, M, cache.D))
+    qp = _kv_need(h, q, "q", (Hq, M, cache.D))
     s = _kv_stream(h, cache, batch, stream)
-    out = torch.empty(M, Hq * D, dtype=torch.bfloat16, device=q.device) if out is None else out
-    _kv_need(h, out, "out", (M, Hq * D))
-    _kv_need(h, lse, "lse", (Hq, M), torch.float32)
-    st = lib().fnl_paged_attention(h.ptr, s, cache.c, batch.c, M, Hq, _p(q), D ** -0.5 if scale is None else scale,
-                                   window, sinks, _p(out), _p(lse))
+    if out is None:
+        out = torch.empty((M, Hq * D), dtype=torch.bfloat16, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _kv_need(h, out, "out", (M, Hq * D))
+    lp = None if lse is None else _kv_need(h, lse, "lse", (Hq, M), torch.float32)
+    st = lib().fnl_paged_attention(h.ptr, s, cache.ptr, batch.ptr, M, Hq, qp, D ** -0.5 if scale is None else scale, window,
+                                   sinks, op, lp)
     if st != FNL_OK:
         h._raise(st, "fnl_paged_attention")
     return {"out": out, "lse": lse}
