@@ -143,13 +143,18 @@ int qkv_columns(int Hq, int Hkv, int D) {
   return n <= kMaxN ? static_cast<int>(n) : 0;
 }
 
-// Paged-cache block: status word, one arrival counter and two partial-sum slots
-// per block of the attention kernel's split form (two blocks an SM at most).
+// Paged-cache block: status word, one arrival counter per block, the tensor-core
+// form's two work counters, then two partial-sum slots
+// per block of the attention kernels (the split form has two blocks an SM at most,
+// the tensor-core form one, with larger slots).
 constexpr int kKvBlocksPerSm = 2;
-size_t kv_fixed_bytes(const fnl_handle* h) { return kStatusBytes + static_cast<size_t>(h->num_sms) * kKvBlocksPerSm * 4; }
+size_t kv_claim_offset(const fnl_handle* h) { return kStatusBytes + static_cast<size_t>(h->num_sms) * kKvBlocksPerSm * 4; }
+size_t kv_fixed_bytes(const fnl_handle* h) { return kv_claim_offset(h) + 8; }
 size_t kv_part_offset(const fnl_handle* h) { return (kv_fixed_bytes(h) + 255) & ~static_cast<size_t>(255); }
 size_t kv_ws_bytes(const fnl_handle* h) {
-  return kv_part_offset(h) + static_cast<size_t>(h->num_sms) * kKvBlocksPerSm * 2 * fnl::k8::kPartFloats * 4;
+  const size_t split = static_cast<size_t>(kKvBlocksPerSm) * 2 * fnl::k8::kPartFloats * 4;
+  const size_t prompt = static_cast<size_t>(2) * fnl::k9::kPartFloats * 4;
+  return kv_part_offset(h) + h->num_sms * std::max(split, prompt);
 }
 
 size_t align256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
@@ -1160,7 +1165,7 @@ fnl_status fnl_create(fnl_handle** out, int device, const fnl_options* opt) {
   }
   fnl_status st = ensure_workspace(h, nullptr, need);
   if (st == FNL_OK && (cudaMalloc(&h->kv_ws, kv_ws_bytes(h)) != cudaSuccess ||
-                       cudaMemset(h->kv_ws, 0, kv_ws_bytes(h)) != cudaSuccess))
+                       cudaMemset(h->kv_ws, 0, kv_fixed_bytes(h)) != cudaSuccess))
     st = FNL_ERR_CUDA;
   if (st != FNL_OK) {
     if (h->ws) cudaFree(h->ws);
@@ -1564,16 +1569,17 @@ fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a
     return fail(h, FNL_ERR_UNSUPPORTED, "the paged attention kernel was built with %d registers a thread", regs);
   Params p{};
   p.a = a;
+  p.claim = reinterpret_cast<unsigned*>(h->kv_ws + kv_claim_offset(h));
   if (h->opt.debug_stall_calls > 0) {   // fault injection for the status-path tests
     p.stall = 1;
     --h->opt.debug_stall_calls;
   }
-  const long long tiles = (static_cast<long long>(a.kv.max_q) * a.group + ROWS - 1) / ROWS;
+  if (a.kv.B > kMaxSeqs) return fail(h, FNL_ERR_UNSUPPORTED, "B=%d exceeds %d", a.kv.B, kMaxSeqs);
   char buf[160];
-  snprintf(buf, sizeof(buf), "paged attention, tensor-core form, grid %lld x %d x %d", tiles, a.kv.Hkv, a.kv.B);
+  snprintf(buf, sizeof(buf), "paged attention, tensor-core form, grid %d", h->num_sms);
   h->plan_text = buf;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles), a.kv.Hkv, a.kv.B);
+  cfg.gridDim = dim3(static_cast<unsigned>(h->num_sms));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = Cfg<D>::SMEM;
   cfg.stream = s;

@@ -2,27 +2,42 @@
 // cores. The mathematics, the row order (token by token, the heads of a group
 // side by side) and the masks are K8's.
 //
-// A block owns 256 rows of one sequence and key head as two tiles of 128 that
-// take turns: while the tensor pipe works on one tile's products, the other
-// tile's softmax runs. Per 128 keys and tile: S = Q K^T into TMEM (both operands
-// from shared memory, fp32), one thread per row reads its 128 scores, writes the
-// probabilities back over them as packed bf16, and O += P V with P read from
-// TMEM as the A operand and V from shared memory as it was loaded (rows = keys,
-// the transposed-B form), so neither S nor P touches shared memory. TMEM: two S
-// tiles of 128 columns and two O tiles of D.
+// A piece of work is a part of the key tiles of 256 rows of one sequence and key
+// head, held as two sub-tiles of 128 rows that take turns: while the tensor pipe
+// works on one sub-tile's products, the other's softmax runs. Per 128 keys and
+// sub-tile: S = Q K^T into TMEM (both operands from shared memory, fp32), one
+// thread per row reads its 128 scores, writes the probabilities back over them as
+// packed bf16, and O += P V with P read from TMEM as the A operand and V from
+// shared memory as it was loaded (rows = keys, the transposed-B form), so neither
+// S nor P touches shared memory. TMEM: two S of 128 columns and two O of D.
 //
-// Roles (12 warps): 0 copies K and V tiles by TMA, page by page, into a ring;
-// 1 issues the products; 4-7 and 8-11 are the two tiles' softmax, which also
-// fetch Q and write the result. A row's accumulators are rescaled only when its
-// maximum has grown by more than 8 (a factor of 256) since the last time: the
-// probabilities stay below 256, exact enough in bf16's and fp32's floating
-// formats, and most key tiles need no pass over O.
+// One block per SM takes row tiles (key head by key head, the longest of a sequence
+// first) from a counter, so that at any time the blocks read the keys and values of
+// few heads, close together: the copies' way through L2 is what a scattered order
+// loses on (ragged prompts ran 1.8 times longer with the heads side by side). Whole
+// tiles only fill whole waves; the (row tile, key tile) units of the rest, or of all
+// when there are fewer tiles than SMs, are dealt evenly over the blocks. A block's
+// first and last pieces of those may be parts: they leave fp32 partial sums, and the
+// last block to arrive adds them in block order. Which block takes a whole tile does
+// not touch its result, and the parts are cut by block number, so results do not
+// depend on the order of arrival.
 //
-// Tensor bound by design: a key tile costs 4 * 128 * 128 * D multiply-adds on the
-// tensor pipe (2048 cycles at D = 128) against 2 * 128 * 128 exponentials on the
-// special-function units (2048 cycles).
+// Roles (12 warps): 0 takes pieces of work, announces them to the others through a
+// two-entry queue and copies K and V tiles by TMA, page by page, into a ring;
+// 1 issues the products; 2 and 3 fetch the next piece's Q; 4-7 and 8-11 are the two
+// sub-tiles' softmax, which also write the result. The first half of a tile's
+// probabilities is handed to the second product while the other half is computed.
+// A row's accumulators are rescaled only when its maximum has grown by more than 8
+// (a factor of 256) since the last time: the probabilities stay below 256, exact
+// enough in bf16's and fp32's floating formats, and most key tiles need no pass
+// over O.
 //
-// Slots that no row of the block sees are not copied (whole pages) or are zeroed
+// Bound: a key tile costs 4 * 128 * 128 * D multiply-adds on the tensor pipe (2048
+// cycles at D = 128) and 2 * 128 * 128 exponentials, 2048 cycles on the
+// special-function units alone; so a part of them is computed on the FMA pipe
+// (exp2_fma).
+//
+// Slots that no row of the piece sees are not copied (whole pages) or are zeroed
 // in V's tile before the product (rows), since 0 * NaN would reach the result;
 // their scores are replaced, not added to.
 #pragma once
@@ -83,37 +98,126 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Three-input maximum.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer (added to
+// 1.5 * 2^23 it sits in the low bits) and |f| <= 1/2, 2^f by the polynomial of degree
+// 4 whose largest relative error is least (Remez exchange: 2.6e-6), n added to the
+// exponent. x is held at -126 from below (the result is then 2^-126 or less).
+__device__ __forceinline__ f32x2 exp2_fma(f32x2 x) {
+  float a, b;
+  unpk2(x, a, b);
+  x = pk2(fmaxf(a, -126.f), fmaxf(b, -126.f));
+  const f32x2 magic = pk2(12582912.f, 12582912.f);
+  const f32x2 t = add2(x, magic);
+  const f32x2 f = sub2(x, sub2(t, magic));
+  f32x2 y = fma2(f, pk2(0.00957010221f, 0.00957010221f), pk2(0.0559178591f, 0.0559178591f));
+  y = fma2(f, y, pk2(0.240247443f, 0.240247443f));
+  y = fma2(f, y, pk2(0.693121791f, 0.693121791f));
+  y = fma2(f, y, pk2(0.999999285f, 0.999999285f));
+  float t0, t1, y0, y1;
+  unpk2(t, t0, t1);
+  unpk2(y, y0, y1);
+  return pk2(__int_as_float(__float_as_int(y0) + (__float_as_int(t0) << 23)),
+             __int_as_float(__float_as_int(y1) + (__float_as_int(t1) << 23)));
+}
+
 namespace k9 {
 
 constexpr int WARPS = 12;
 constexpr int THREADS = WARPS * 32;
 constexpr int TILE = 128;              // keys of a tile, rows of a sub-tile
 constexpr int ROWS = 2 * TILE;
-constexpr int REG_SOFTMAX = 208, REG_OTHER = 72;   // 256 * 208 + 128 * 72 <= 384 * 168, the launch's registers
+constexpr int REG_SOFTMAX = 208, REG_OTHER = 80;   // 256 * 208 + 128 * 80 <= 384 * 168, the launch's registers
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float GROWTH = 8.f;          // rescale when the maximum (base 2) has grown by more
+constexpr int FMA_EVERY = 0;           // one pair of exponentials in so many goes to the FMA pipe (0: none)
+constexpr int kMaxSeqs = 32768;        // the plan's prefix sums fit the ring
+constexpr int CTRL_BYTES = 2048;
+constexpr int kPartFloats = ROWS * (128 + 2);   // of one slot: accumulators, maximum, sum
 
 template <int D>
 struct Cfg {
   static constexpr int HALVES = D / 64;
   static constexpr int TILE_BYTES = TILE * D * 2;   // Q sub-tile, K tile, V tile: HALVES blocks of 128 x 64
   static constexpr int HALF_BYTES = TILE * 128;
-  static constexpr int STAGES = D == 128 ? 5 : 8;
-  static constexpr int SMEM = 2 * TILE_BYTES + STAGES * TILE_BYTES + 1024 + 256;
+  static constexpr int STAGES = D == 128 ? 5 : 10;
+  static constexpr int SMEM = 2 * TILE_BYTES + STAGES * TILE_BYTES + 1024 + CTRL_BYTES;
   static constexpr uint32_t S0 = 0, O0 = 256;       // TMEM columns: S at 0 and 128 (P over it), O at 256 and 256 + D
-};
-
-struct Ctrl {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full[2], q_full, drain;
-  uint32_t tmem_base;
-  uint32_t armed, armed_parity;   // ring slots with a copy issued, and the parity of each one's last
-  int abort_flag;
+  static_assert((kMaxSeqs + 1) * 4 <= STAGES * TILE_BYTES, "prefix sums in the ring");
 };
 
 struct Params {
   AttnParams a;
+  unsigned* claim;   // whole tiles taken beyond the first wave; blocks that have ended. Both zero between launches
   int stall;   // fault injection for the status-path tests: block 0 withholds its first key tile
 };
+
+// A row tile: 256 rows of a sequence (one key head) and its key tiles, the union
+// of what its rows see: tiles that hold sinks, then those from the window on.
+struct RowTile {
+  int first, n, rows, pos_first;   // the sequence's rows in the batch, its new tokens, rows and first position
+  int r0;
+  int lo_tile, sink_tiles, n0, n1; // key tiles that the two sub-tiles reach: the first n0, n1 of the list
+  k8::Sight sight;
+  __device__ __forceinline__ int tiles() const { return max(max(n0, n1), 1); }   // one at least writes the rows
+  __device__ __forceinline__ int key_of(int i) const { return (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE; }
+};
+__device__ __forceinline__ RowTile row_tile(const AttnParams& p, int b, int j) {
+  const KvSeq q = kv_seq(p.kv, b);
+  RowTile t;
+  t.first = q.first;
+  t.n = q.n;
+  t.rows = q.n * p.group;
+  t.pos_first = q.len - q.n;
+  t.r0 = j * ROWS;
+  k8::Sight& s = t.sight;
+  s.pos0 = t.pos_first + t.r0 / p.group;
+  s.last = t.pos_first + (min(t.r0 + ROWS, t.rows) - 1) / p.group;
+  s.rows = t.rows;
+  s.group = p.group;
+  s.len = min(q.len, s.last + 1);
+  s.window = p.window;
+  s.sinks = p.sinks;
+  s.lo = p.window > 0 ? max(0, s.pos0 - p.window + 1) : 0;
+  t.lo_tile = s.lo / TILE;
+  t.sink_tiles = min((min(p.sinks, max(s.len, 0)) + TILE - 1) / TILE, t.lo_tile);
+  auto reach = [&](int first) {
+    if (first >= t.rows) return 0;
+    const int end = min(q.len, t.pos_first + (min(first + TILE, t.rows) - 1) / p.group + 1);
+    return end > 0 ? t.sink_tiles + (end + TILE - 1) / TILE - t.lo_tile : 0;
+  };
+  t.n0 = reach(t.r0);
+  t.n1 = reach(t.r0 + TILE);
+  return t;
+}
+__device__ __forceinline__ int row_tiles(const AttnParams& p, int b) {
+  return (kv_seq(p.kv, b).n * p.group + ROWS - 1) / ROWS;
+}
+
+// A piece of work: key tiles [t0, t1) of a row tile for one key head; t1 = 0: the end.
+// Parts of a tile shared by the blocks c0 .. c1.
+struct Piece {
+  RowTile t;
+  int head, t0, t1, c0, c1;
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == t.tiles(); }
+};
+
+struct Ctrl {
+  uint64_t full[10], empty[10], s_full[2], p_half[2][2], o_full[2], q_full, q_empty, work_full[2], work_empty[2], join, drain;
+  uint32_t tmem_base;
+  uint32_t armed, armed_parity;   // ring slots with a copy issued, and the parity of each one's last
+  int abort_flag;
+  int scan[WARPS];
+  int found[2];                   // the block's first shared tile, units before it
+  int last;                       // this block arrived last at a shared piece
+  Piece piece[2];
+};
+static_assert(sizeof(Ctrl) <= CTRL_BYTES, "the control block");
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -126,6 +230,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* ring = smem + 2 * C::TILE_BYTES;
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(ring + C::STAGES * C::TILE_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abortf = &ctrl->abort_flag;
+  int* status = p.kv.status;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -134,53 +240,108 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctrl->s_full[s], 1);
-      mbar_init(&ctrl->p_full[s], 4);
+      mbar_init(&ctrl->p_half[s][0], 4);
+      mbar_init(&ctrl->p_half[s][1], 4);
       mbar_init(&ctrl->o_full[s], 1);
     }
-    mbar_init(&ctrl->q_full, 8);
+    mbar_init(&ctrl->q_full, 2);
+    mbar_init(&ctrl->q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctrl->work_full[s], 1);
+      mbar_init(&ctrl->work_empty[s], 11);   // the warps that read the queue
+    }
+    mbar_init(&ctrl->join, 8);
     mbar_init(&ctrl->drain, 1);
     ctrl->abort_flag = 0;
     fence_mbar_init();
   }
   pdl_wait();
-  const int b = blockIdx.z, head = blockIdx.y;
-  const KvSeq seq = kv_seq(p.kv, b);
-  const int rows = seq.n * p.group;
-  const int r0 = (static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)) * ROWS;   // the longest first
-  if (r0 >= rows) return;
+
+  // ---- the plan: prefix sums of the sequences' row tiles, then of the row tiles' key tiles
+  int* first_tile = reinterpret_cast<int*>(ring);   // [B + 1] row tiles before each sequence
+  auto block_scan = [&](int v, int& total) {        // inclusive scan over the block's threads
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) ctrl->scan[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += ctrl->scan[w];
+      all += ctrl->scan[w];
+    }
+    total = all;
+    return x + before;
+  };
+  const int B = p.kv.B;
+  int R = 0;
+  for (int i = 0; i < B; i += THREADS) {
+    const int b = i + threadIdx.x;
+    int total;
+    const int x = block_scan(b < B ? row_tiles(p, b) : 0, total);
+    if (b < B) first_tile[b + 1] = R + x;
+    R += total;
+  }
+  if (threadIdx.x == 0) first_tile[0] = 0;
+  __syncthreads();
+  auto seq_of = [&](int r) {   // sequence of row tile r: the last whose first row tile is at most r
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first_tile[mid] <= r) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
+  // tiles: N = Hkv R in the order (head, sequence, row tile from the last down). The
+  // first W, whole waves of them, are taken whole; the rest are shared.
+  const long long N = static_cast<long long>(R) * p.kv.Hkv;
+  const int G = gridDim.x;
+  const long long W = N / G * G;
+  const int rest = static_cast<int>(N - W);   // < G <= THREADS
+  int units_rest, my_tiles = 0;
+  if (static_cast<int>(threadIdx.x) < rest) {
+    const int r = static_cast<int>((W + threadIdx.x) % R), b = seq_of(r);
+    my_tiles = row_tile(p, b, first_tile[b + 1] - 1 - r).tiles();   // (r counts down inside a sequence)
+  }
+  const int my_end = block_scan(my_tiles, units_rest);
+  // at least four key tiles a block, unless there are more tiles than that makes blocks
+  const int Gr = rest == 0 ? 0 : min(G, max(rest, units_rest / 4));
+  const bool shares = static_cast<int>(blockIdx.x) < Gr;
+  const int u0 = shares ? static_cast<int>(static_cast<long long>(blockIdx.x) * units_rest / Gr) : 0;
+  const int u1 = shares ? static_cast<int>(static_cast<long long>(blockIdx.x + 1) * units_rest / Gr) : 0;
+  if (shares && my_tiles > 0 && my_end > u0 && my_end - my_tiles <= u0) {
+    ctrl->found[0] = threadIdx.x;
+    ctrl->found[1] = my_end - my_tiles;
+  }
   if (warp == 1) {
     tmem_alloc(&ctrl->tmem_base, TMEM_COLS);
     tmem_relinquish();
   }
+  fence_proxy_async_smem();   // the plan's stores into the ring come before its bulk copies
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
-  volatile int* abortf = &ctrl->abort_flag;
-  int* status = p.kv.status;
 
-  // ---- what the block's rows see
-  const int pos_first = seq.len - seq.n;                     // position of the sequence's first new token
-  k8::Sight sight;
-  sight.pos0 = pos_first + r0 / p.group;
-  sight.last = pos_first + (min(r0 + ROWS, rows) - 1) / p.group;
-  sight.rows = rows;
-  sight.group = p.group;
-  sight.len = min(seq.len, sight.last + 1);
-  sight.window = p.window;
-  sight.sinks = p.sinks;
-  sight.lo = p.window > 0 ? max(0, sight.pos0 - p.window + 1) : 0;
-  const int lo_tile = sight.lo / TILE;
-  const int sink_tiles = min((min(p.sinks, max(sight.len, 0)) + TILE - 1) / TILE, lo_tile);
-  auto key_of = [&](int i) { return (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE; };
-  // key tiles of each sub-tile: the second one's rows reach further
-  auto tiles_of = [&](int s) {
-    const int first = r0 + s * TILE;
-    if (first >= rows) return 0;
-    const int end = min(seq.len, pos_first + (min(first + TILE, rows) - 1) / p.group + 1);
-    return end > 0 ? sink_tiles + (end + TILE - 1) / TILE - lo_tile : 0;
+  // The other roles' side of the queue: the next piece (null when the wait gives up),
+  // and its release.
+  uint32_t taken = 0;
+  auto take = [&]() -> const Piece* {
+    const int q = taken & 1;
+    if (!warp_wait(&ctrl->work_full[q], (taken >> 1) & 1, abortf, status, kStatusWaitFull, p.wait_ns)) return nullptr;
+    return &ctrl->piece[q];
   };
-  const int n0 = tiles_of(0), n1 = tiles_of(1), n = max(n0, n1);
+  auto release = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctrl->work_empty[taken & 1]);
+    ++taken;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies
@@ -191,37 +352,108 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int part = lane / C::HALVES, half = lane % C::HALVES;
     int slot = 0;
     uint32_t ph = 0, armed = 0, parity = 0;
-    bool withhold = prm.stall != 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+    bool withhold = prm.stall != 0 && blockIdx.x == 0;
     bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      const int key = key_of(i) + part * bp;
-      int id = -1;
-      if (lane < copies && key < sight.len && (key + bp > sight.lo || key < sight.sinks)) id = kv_page(p.kv, b, key);
-      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * bp * 128;
-      const int row = kv_row_in_page(p.kv, head, key);
-      for (int kv = 0; kv < 2; ++kv) {
-        ok = warp_wait(&ctrl->empty[slot], ph ^ 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
-        if (!ok) break;
-        if (withhold) {
-          withhold = false;
-        } else {
-          if (lane == 0) {
-            if (bytes) mbar_arrive_expect_tx(&ctrl->full[slot], bytes);
-            else mbar_arrive(&ctrl->full[slot]);
-          }
-          __syncwarp();
-          if (id >= 0)
-            tma_load_3d(smem_u32(ring) + slot * C::TILE_BYTES + half * C::HALF_BYTES + part * bp * 128,
-                        kv ? &tm_v : &tm_k, &ctrl->full[slot], half * 64, row, id);
-          armed |= 1u << slot;
-          parity = (parity & ~(1u << slot)) | (ph << slot);
+    uint32_t sent = 0;
+    int at_head = 0, at_b = 0, at_r = 0;   // the last tile taken: its head and sequence, row tiles before that sequence
+    // Tile `idx` for the whole warp: 32 sequences at a time from the last one on.
+    auto find = [&](long long idx, int& head, int& b, int& j) {
+      head = static_cast<int>(idx / R);
+      const int r = static_cast<int>(idx - static_cast<long long>(head) * R);
+      if (head != at_head || r < at_r) at_b = at_r = 0;
+      at_head = head;
+      while (at_b < B) {
+        const int mine = at_b + lane < B ? row_tiles(p, at_b + lane) : 0;
+        int x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
         }
-        if (++slot == C::STAGES) {
-          slot = 0;
-          ph ^= 1u;
+        const unsigned behind = __ballot_sync(0xffffffffu, at_r + x > r);
+        if (behind) {
+          const int l = __ffs(behind) - 1;
+          const int end = at_r + __shfl_sync(0xffffffffu, x, l), n = __shfl_sync(0xffffffffu, mine, l);
+          at_b += l;
+          at_r = end - n;
+          b = at_b;
+          j = end - 1 - r;
+          return;
+        }
+        at_r += __shfl_sync(0xffffffffu, x, 31);
+        at_b += 32;
+      }
+      b = j = at_b = at_r = 0;   // the batch's arrays have changed under the kernel: any tile will do
+    };
+    // Announces a piece (t1 < 0: to the tile's end) and copies its tiles.
+    auto serve = [&](int head, int b, int j, int t0, int t1, int c0, int c1) {
+      const int q = sent & 1;
+      ok = warp_wait(&ctrl->work_empty[q], ((sent >> 1) & 1) ^ 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
+      if (!ok) return;
+      Piece& w = ctrl->piece[q];
+      if (lane == 0) {
+        if (t1 != 0) w.t = row_tile(p, b, j);
+        w.head = head;
+        w.t0 = t0;
+        w.t1 = t1 < 0 ? w.t.tiles() : t1;
+        w.c0 = c0;
+        w.c1 = c1;
+        mbar_arrive(&ctrl->work_full[q]);
+      }
+      __syncwarp();
+      ++sent;
+      t1 = w.t1;
+      const k8::Sight sight = w.t.sight;
+      const int lo_tile = w.t.lo_tile, sink_tiles = w.t.sink_tiles;
+      for (int i = t0; i < t1 && ok; ++i) {
+        const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE + part * bp;
+        int id = -1;
+        if (lane < copies && key < sight.len && (key + bp > sight.lo || key < sight.sinks)) id = kv_page(p.kv, b, key);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * bp * 128;
+        const int row = kv_row_in_page(p.kv, head, key);
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = warp_wait(&ctrl->empty[slot], ph ^ 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
+          if (!ok) break;
+          if (withhold) {
+            withhold = false;
+          } else {
+            if (lane == 0) {
+              if (bytes) mbar_arrive_expect_tx(&ctrl->full[slot], bytes);
+              else mbar_arrive(&ctrl->full[slot]);
+            }
+            __syncwarp();
+            if (id >= 0)
+              tma_load_3d(smem_u32(ring) + slot * C::TILE_BYTES + half * C::HALF_BYTES + part * bp * 128,
+                          kv ? &tm_v : &tm_k, &ctrl->full[slot], half * 64, row, id);
+            armed |= 1u << slot;
+            parity = (parity & ~(1u << slot)) | (ph << slot);
+          }
+          if (++slot == C::STAGES) {
+            slot = 0;
+            ph ^= 1u;
+          }
         }
       }
+    };
+    int head, b, j;
+    for (long long idx = blockIdx.x; ok && idx < W;) {   // whole tiles: the first by block number, then as they come
+      find(idx, head, b, j);
+      serve(head, b, j, 0, -1, 0, 0);
+      unsigned got = 0;
+      if (lane == 0) got = atomicAdd(prm.claim, 1u);
+      idx = static_cast<long long>(G) + __shfl_sync(0xffffffffu, got, 0);
     }
+    if (shares) {
+      int tile = ctrl->found[0], base = ctrl->found[1];
+      for (int u = u0; ok && u < u1; ++tile) {
+        find(W + tile, head, b, j);
+        const int n = row_tile(p, b, j).tiles();
+        serve(head, b, j, u - base, min(u1 - base, n), unit_owner(base, Gr, units_rest), unit_owner(base + n - 1, Gr, units_rest));
+        base += n;
+        u = base;
+      }
+    }
+    if (ok) serve(0, 0, 0, 0, 0, 0, 0);   // the end
     if (lane == 0) {
       ctrl->armed = armed;
       ctrl->armed_parity = parity;
@@ -232,32 +464,35 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr uint32_t idesc_qk = idesc_bf16(TILE, TILE);
     constexpr uint32_t idesc_pv = idesc_bf16(TILE, D) | (1u << 16);   // B rows are keys: transposed
     int slot = 0;
-    uint32_t ph = 0;
+    uint32_t ph = 0, pieces = 0, done[2] = {0, 0};   // done: tiles of each sub-tile so far, over all pieces
     auto advance = [&]() {
       if (++slot == C::STAGES) {
         slot = 0;
         ph ^= 1u;
       }
     };
+    // descriptors differ in their address field alone (16-byte units)
+    const uint64_t kmajor = sw128_desc(0), nmajor = sw128_mn_desc(0, C::HALF_BYTES);
+    const uint32_t q16 = smem_u32(smem) >> 4, ring16 = smem_u32(ring) >> 4;
     auto qk = [&](int s, int at) {
       if (lane == 0) {
-        const uint32_t q = smem_u32(smem) + s * C::TILE_BYTES, k = smem_u32(ring) + at * C::TILE_BYTES;
+        const uint64_t q = kmajor + q16 + s * (C::TILE_BYTES >> 4), k = kmajor + ring16 + at * (C::TILE_BYTES >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * C::HALF_BYTES + (kk & 3) * 32;
-          umma_bf16(tmem + C::S0 + s * TILE, sw128_desc(q + o), sw128_desc(k + o), idesc_qk, kk > 0);
+          const uint32_t o = ((kk >> 2) * C::HALF_BYTES + (kk & 3) * 32) >> 4;
+          umma_bf16(tmem + C::S0 + s * TILE, q + o, k + o, idesc_qk, kk > 0);
         }
         umma_commit(&ctrl->s_full[s]);
       }
       __syncwarp();
     };
-    auto pv = [&](int s, int at, bool first) {
+    auto pv = [&](int s, int at, int h, bool first) {   // half h of the keys
       if (lane == 0) {
-        const uint32_t v = smem_u32(ring) + at * C::TILE_BYTES;
+        const uint64_t v = nmajor + ring16 + at * (C::TILE_BYTES >> 4) + h * (TILE / 2 * 128 >> 4);
+        const uint32_t o = tmem + C::O0 + s * D, a = tmem + C::S0 + s * TILE + h * (TILE / 4);
 #pragma unroll
-        for (int kk = 0; kk < TILE / 16; ++kk)
-          umma_bf16_ts(tmem + C::O0 + s * D, tmem + C::S0 + s * TILE + kk * 8, sw128_mn_desc(v + kk * 2048, C::HALF_BYTES),
-                       idesc_pv, !first || kk > 0);
+        for (int kk = 0; kk < TILE / 32; ++kk)
+          umma_bf16_ts(o, a + kk * 8, v + kk * (2048 >> 4), idesc_pv, !first || h > 0 || kk > 0);
       }
       __syncwarp();
     };
@@ -265,57 +500,71 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) umma_commit(bar);
       __syncwarp();
     };
-    bool ok = n == 0 || (warp_wait(&ctrl->q_full, 0, abortf, status, kStatusWaitConv, p.wait_ns) &&
-                         warp_wait(&ctrl->full[slot], ph, abortf, status, kStatusWaitFull, p.wait_ns));
-    if (ok && n > 0) {
-      tc_fence_after();
-      if (n0 > 0) qk(0, slot);
-      if (n1 > 0) qk(1, slot);
-      commit(&ctrl->empty[slot]);
-      advance();
-    }
-    for (int i = 0; i < n && ok; ++i) {
-      // V of tile i at `slot`, K of tile i + 1 behind it
-      const int vs = slot;
-      ok = warp_wait(&ctrl->full[slot], ph, abortf, status, kStatusWaitFull, p.wait_ns);
+    auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+      const bool r = warp_wait(bar, parity & 1u, abortf, status, code, p.wait_ns);
+      if (r) tc_fence_after();
+      return r;
+    };
+    bool ok = true;
+    while (ok) {
+      const Piece* w = take();
+      ok = w != nullptr;
+      if (!ok || w->t1 == 0) break;
+      const int reach[2] = {w->t.n0, w->t.n1};
+      const k8::Sight sight = w->t.sight;
+      const int t0 = w->t0, t1 = w->t1, lo_tile = w->t.lo_tile, sink_tiles = w->t.sink_tiles;
+      release();
+      ok = wait(&ctrl->q_full, pieces++, kStatusWaitConv) && wait(&ctrl->full[slot], ph, kStatusWaitFull);
       if (!ok) break;
-      const int key = key_of(i);
-      if (key + TILE > sight.len || (key < sight.lo && key + TILE > sight.sinks)) {
-        // rows of V that nobody sees become zeros (a warp instruction covers 4 rows' halves)
-        for (int r = lane >> 3; r < TILE; r += 4)
-          if (!sight.any(key + r))
-            for (int h = 0; h < C::HALVES; ++h)
-              st_shared_v4(smem_u32(ring) + vs * C::TILE_BYTES + h * C::HALF_BYTES + r * 128 + (lane & 7) * 16,
-                           make_uint4(0, 0, 0, 0));
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
+      for (int s = 0; s < 2; ++s)
+        if (t0 < reach[s]) qk(s, slot);
+      commit(&ctrl->empty[slot]);
+      if (t1 - t0 == 1) commit(&ctrl->q_empty);
       advance();
-      const int ks = slot;
-      bool have_k = false;
-      for (int s = 0; s < 2 && ok; ++s) {
-        const int ns = s ? n1 : n0;
-        if (i < ns) {
-          ok = warp_wait(&ctrl->p_full[s], i & 1, abortf, status, kStatusWaitConv, p.wait_ns);
-          if (!ok) break;
-          tc_fence_after();
-          pv(s, vs, i == 0);
-          if (i + 1 == ns) commit(&ctrl->o_full[s]);
+      for (int i = t0; i < t1 && ok; ++i) {
+        // V of tile i at `slot`, K of tile i + 1 behind it
+        const int vs = slot;
+        ok = wait(&ctrl->full[slot], ph, kStatusWaitFull);
+        if (!ok) break;
+        const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
+        if (key + TILE > sight.len || (key < sight.lo && key + TILE > sight.sinks)) {
+          // rows of V that nobody sees become zeros (a warp instruction covers 4 rows' halves)
+          for (int r = lane >> 3; r < TILE; r += 4)
+            if (!sight.any(key + r))
+              for (int h = 0; h < C::HALVES; ++h)
+                st_shared_v4(smem_u32(ring) + vs * C::TILE_BYTES + h * C::HALF_BYTES + r * 128 + (lane & 7) * 16,
+                             make_uint4(0, 0, 0, 0));
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        if (s == 1) commit(&ctrl->empty[vs]);
-        if (i + 1 < ns) {
-          if (!have_k) {
-            ok = warp_wait(&ctrl->full[ks], ph, abortf, status, kStatusWaitFull, p.wait_ns);
-            if (!ok) break;
-            tc_fence_after();
-            have_k = true;
-          }
-          qk(s, ks);
-        }
-      }
-      if (ok && i + 1 < n) {
-        commit(&ctrl->empty[ks]);
         advance();
+        const int ks = slot;
+        bool have_k = false;
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (i < reach[s]) {
+            for (int h = 0; h < 2 && ok; ++h) {
+              ok = wait(&ctrl->p_half[s][h], done[s], kStatusWaitConv);
+              if (ok) pv(s, vs, h, i == t0);
+            }
+            if (!ok) break;
+            ++done[s];
+            if (i + 1 == min(t1, reach[s])) commit(&ctrl->o_full[s]);
+          }
+          if (s == 1) commit(&ctrl->empty[vs]);
+          if (i + 1 < t1 && i + 1 < reach[s]) {
+            if (!have_k) {
+              ok = wait(&ctrl->full[ks], ph, kStatusWaitFull);
+              if (!ok) break;
+              have_k = true;
+            }
+            qk(s, ks);
+          }
+        }
+        if (ok && i + 1 < t1) {
+          commit(&ctrl->empty[ks]);
+          if (i + 2 == t1) commit(&ctrl->q_empty);
+          advance();
+        }
       }
     }
     if (!ok || *abortf) {   // every product issued is done before TMEM is freed
@@ -324,132 +573,248 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
     }
   } else if (warp < 4) {
+    // ------------------------------------------------------------ Q
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_OTHER));
-  } else {
-    // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
-    const int s = (warp - 4) >> 2, quarter = warp & 3;
-    const int r = r0 + s * TILE + quarter * 32 + lane;       // this thread's row
-    {   // Q: the 8 warps fetch 256 rows, 16 bytes a lane, into the swizzled tiles
-      constexpr int CH = D / 8;
-      const int t = threadIdx.x - 128;
+    constexpr int CH = D / 8, STEP = 64 / CH;   // 16-byte chunks of a row; rows of one turn of the 64 threads
+    const int t = threadIdx.x - 64, c = t % CH;
+    uint32_t pieces = 0;
+    bool ok = true;
+    while (ok) {
+      const Piece* w = take();
+      ok = w != nullptr;
+      if (!ok || w->t1 == 0) break;
+      const int r0 = w->t.r0, rows = w->t.rows, first = w->t.first, head0 = w->head * p.group;
+      release();
+      if (pieces > 0) ok = warp_wait(&ctrl->q_empty, (pieces - 1) & 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
+      if (!ok) break;
+      ++pieces;
+      int row = t / CH;
+      int token = first + (r0 + row) / p.group, hq = (r0 + row) % p.group;
+      const int dt = STEP / p.group, dh = STEP % p.group;
 #pragma unroll 4
-      for (int idx = t; idx < ROWS * CH; idx += 256) {
-        const int row = idx / CH, c = idx % CH;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r0 + row < rows) x = ldg16(p.q + k8::q_row(p, seq.first, head, r0 + row) * D + c * 8);
-        st_shared_v4(smem_u32(smem) + (row / TILE) * C::TILE_BYTES + (c >> 3) * C::HALF_BYTES + (row % TILE) * 128 +
-                         (((c & 7) ^ (row & 7)) << 4),
-                     x);
+      for (; row < ROWS; row += STEP) {
+        const bool in = r0 + row < rows;
+        const bf16* src = in ? p.q + (static_cast<long long>(head0 + hq) * p.kv.M + token) * D + c * 8 : p.q;
+        k8::cp16(smem_u32(smem) + (row / TILE) * C::TILE_BYTES + (c >> 3) * C::HALF_BYTES + (row % TILE) * 128 +
+                     (((c & 7) ^ (row & 7)) << 4),
+                 src, in ? 16 : 0);
+        token += dt;
+        hq += dh;
+        if (hq >= p.group) {
+          hq -= p.group;
+          ++token;
+        }
       }
+      k8::cp_commit();
+      k8::cp_wait<0>();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->q_full);
     }
-    const int ns = s ? n1 : n0;
-    const int pos = pos_first + min(r, rows - 1) / p.group;
-    // the warp's own span of positions, for its masks
-    k8::Sight mine = sight;
-    mine.pos0 = pos_first + min(r0 + s * TILE + quarter * 32, rows - 1) / p.group;
-    mine.last = pos_first + min(r0 + s * TILE + quarter * 32 + 31, rows - 1) / p.group;
+  } else {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
+    const int s = (warp - 4) >> 2, quarter = warp & 3;
+    const int row = s * TILE + quarter * 32 + lane;          // this thread's row of the 256
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + lanes + C::S0 + s * TILE, to = tmem + lanes + C::O0 + s * D;
     const float scale = p.scale_log2;
-    float top = -INFINITY;   // the maximum that the sum and the accumulators are relative to
-    f32x2 sum2 = pk2(0.f, 0.f);
+    uint32_t done = 0, outs = 0;   // tiles and pieces of this sub-tile so far
+    uint32_t joins = 0;
+    auto join = [&]() {            // a bounded barrier of the 8 softmax warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->join);
+      return warp_wait(&ctrl->join, joins++ & 1u, abortf, status, kStatusWaitDrain, p.wait_ns);
+    };
     bool ok = true;
-    for (int i = 0; i < ns; ++i) {
-      ok = warp_wait(&ctrl->s_full[s], i & 1, abortf, status, kStatusWaitTmemFull, p.wait_ns);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t x[TILE];
+    while (true) {
+      const Piece* w = take();
+      if (w == nullptr || w->t1 == 0) break;
+      const int rows = w->t.rows, r0 = w->t.r0, r = r0 + row;
+      const int t0 = w->t0, end = min(w->t1, s ? w->t.n1 : w->t.n0);
+      const int rr = min(r, rows - 1);
+      const int pos = w->t.pos_first + rr / p.group;
+      // the warp's own span of positions, for its masks
+      const int w0 = w->t.pos_first + min(r0 + s * TILE + quarter * 32, rows - 1) / p.group;
+      const int w1 = w->t.pos_first + min(r0 + s * TILE + quarter * 32 + 31, rows - 1) / p.group;
+      const int lo_tile = w->t.lo_tile, sink_tiles = w->t.sink_tiles;
+      float top = -INFINITY;   // the maximum that the sum and the accumulators are relative to
+      f32x2 sum2 = pk2(0.f, 0.f);
+      for (int i = t0; i < end && ok; ++i, ++done) {
+        ok = warp_wait(&ctrl->s_full[s], done & 1u, abortf, status, kStatusWaitTmemFull, p.wait_ns);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[TILE];
 #pragma unroll
-      for (int c = 0; c < TILE; c += 32) tmem_ld32(ts + c, x + c);
-      tmem_ld_wait();
-      const int key = key_of(i);
-      if (!mine.all(key, TILE)) {
-        const int hi = pos - key, wlo = p.window > 0 ? hi - p.window + 1 : -(1 << 30), sk = p.sinks - key;
+        for (int c = 0; c < TILE; c += 32) tmem_ld32(ts + c, x + c);
+        tmem_ld_wait();
+        const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
+        // some row of the warp does not see some key
+        if (key + TILE - 1 > w0 || (p.window > 0 && key <= w1 - p.window && key + TILE > p.sinks)) {
+          const int hi = pos - key, wlo = p.window > 0 ? hi - p.window + 1 : -(1 << 30), sk = p.sinks - key;
 #pragma unroll
-        for (int c = 0; c < TILE; ++c)
-          if (!(c <= hi && (c >= wlo || c < sk))) x[c] = 0xff800000u;   // -inf
-      }
-      float m = -INFINITY;
+          for (int c = 0; c < TILE; ++c)
+            if (!(c <= hi && (c >= wlo || c < sk))) x[c] = 0xff800000u;   // -inf
+        }
+        float m4[4];
 #pragma unroll
-      for (int c = 0; c < TILE; c += 2) m = fmaxf(m, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
-      m *= scale;
-      if (__any_sync(0xffffffffu, m > top + GROWTH || (top == -INFINITY && m > top))) {
-        const bool grow = m > top + GROWTH || top == -INFINITY;
-        const float f = grow && top != -INFINITY ? k8::ex2(top - m) : 1.f;
-        if (grow) top = m;
-        float a, c;
-        unpk2(sum2, a, c);
-        sum2 = pk2(a * f, c * f);
-        if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {   // (before the first product O holds nothing)
+        for (int c = 0; c < 4; ++c) m4[c] = fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 4]));
 #pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + c0, o);
-            tmem_ld_wait();
+        for (int c = 8; c < TILE; c += 8)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st16(to + c0, o);
+          for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + 4 + e]));
+        const float m = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * scale;
+        if (__any_sync(0xffffffffu, m > top + GROWTH)) {
+          const bool grow = m > top + GROWTH;
+          const float f = grow && top != -INFINITY ? k8::ex2(top - m) : 1.f;
+          if (grow) top = m;
+          float a, c;
+          unpk2(sum2, a, c);
+          sum2 = pk2(a * f, c * f);
+          if (i > t0 && __any_sync(0xffffffffu, f != 1.f)) {   // (before the first product O holds nothing)
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + c0, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(to + c0, o);
+            }
           }
         }
-      }
-      const float base = top == -INFINITY ? 0.f : top;
-      const f32x2 scale2 = pk2(scale, scale), base2 = pk2(-base, -base);
+        const float base = top == -INFINITY ? 0.f : top;
+        const f32x2 scale2 = pk2(scale, scale), base2 = pk2(-base, -base);
+        f32x2 part2 = pk2(0.f, 0.f);
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t w[16];
+        for (int h = 0; h < 4; ++h) {
+          uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const f32x2 t = fma2(pk2(__uint_as_float(x[h * 32 + 2 * c]), __uint_as_float(x[h * 32 + 2 * c + 1])), scale2, base2);
-          float a, d;
-          unpk2(t, a, d);
-          a = k8::ex2(a);
-          d = k8::ex2(d);
-          sum2 = add2(sum2, pk2(a, d));
-          w[c] = pack_bf16x2(a, d);
+          for (int c = 0; c < 16; ++c) {
+            f32x2 y = fma2(pk2(__uint_as_float(x[h * 32 + 2 * c]), __uint_as_float(x[h * 32 + 2 * c + 1])), scale2, base2);
+            float a, d;
+            if (FMA_EVERY > 0 && c % (FMA_EVERY > 0 ? FMA_EVERY : 1) == FMA_EVERY - 1) {
+              y = exp2_fma(y);
+              unpk2(y, a, d);
+            } else {
+              unpk2(y, a, d);
+              a = k8::ex2(a);
+              d = k8::ex2(d);
+              y = pk2(a, d);
+            }
+            if (c & 1) part2 = add2(part2, y);
+            else sum2 = add2(sum2, y);
+            w[c] = pack_bf16x2(a, d);
+          }
+          tmem_st16(ts + h * 16, w);
+          if (h & 1) {   // half the tile's probabilities are in place
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctrl->p_half[s][h >> 1]);
+          }
         }
-        tmem_st16(ts + h * 16, w);
+        sum2 = add2(sum2, part2);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->p_full[s]);
-    }
-    // ---- the result
-    float a, c;
-    unpk2(sum2, a, c);
-    const float sum = a + c;
-    if (ok && ns > 0) {
-      ok = warp_wait(&ctrl->o_full[s], 0, abortf, status, kStatusWaitTmemFull, p.wait_ns);
-      tc_fence_after();
-    }
-    if (ok) {
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const int rr = min(r, rows - 1);
-      const int token = seq.first + rr / p.group, hq = head * p.group + rr % p.group;
+      // ---- the piece's result
+      float a, c;
+      unpk2(sum2, a, c);
+      float sum = a + c;
+      if (ok && t0 < end) {
+        ok = warp_wait(&ctrl->o_full[s], outs & 1u, abortf, status, kStatusWaitTmemFull, p.wait_ns);
+        ++outs;
+        tc_fence_after();
+      }
+      const int token = w->t.first + rr / p.group, hq = w->head * p.group + rr % p.group;
       bf16* dst = p.out + (static_cast<long long>(token) * p.Hq + hq) * D;
+      auto put = [&](int c0, const float (&o)[16], float inv) {   // 16 values of this thread's row
+        float f[8];
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t o[32];
-        if (ns > 0) {
-          tmem_ld32(to + c0, o);
-          tmem_ld_wait();
+        for (int e = 0; e < 16; e += 8) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = o[e + k] * inv;
+          *reinterpret_cast<uint4*>(dst + c0 + e) = pack8(f);
+        }
+      };
+      auto put_lse = [&]() {
+        if (p.lse) p.lse[static_cast<long long>(hq) * p.kv.M + token] = sum > 0.f ? (top + log2f(sum)) * k8::kLn2 : -INFINITY;
+      };
+      const bool whole = w->whole();
+      const int c0 = w->c0, c1 = w->c1;
+      // slot 2i + 1 for a piece that begins in block i, 2i for one begun before; [D / 4][256] float4, maxima, sums
+      auto slot_of = [&](int blk) { return p.part + static_cast<long long>(2 * blk + (blk == c0)) * kPartFloats; };
+      if (ok) {
+        float* mine_part = whole ? nullptr : slot_of(blockIdx.x);
+#pragma unroll
+        for (int d0 = 0; d0 < D; d0 += 16) {
+          uint32_t o[16];
+          float f[16];
+          if (t0 < end) {
+            tmem_ld16(to + d0, o);
+            tmem_ld_wait();
+          }
+          // (a row without keys, and a sub-tile without tiles, have no accumulators)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) f[e] = sum > 0.f ? __uint_as_float(o[e]) : 0.f;
+          if (r < rows) {
+            if (whole) {
+              put(d0, f, sum > 0.f ? 1.f / sum : 0.f);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                __stcg(reinterpret_cast<float4*>(mine_part) + ((d0 + e) >> 2) * ROWS + row,
+                       make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]));
+            }
+          }
         }
         if (r < rows) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = sum > 0.f ? __uint_as_float(o[e + j]) * inv : 0.f;
-            *reinterpret_cast<uint4*>(dst + c0 + e) = pack8(f);
+          if (whole) {
+            put_lse();
+          } else {
+            __stcg(mine_part + ROWS * D + row, top);
+            __stcg(mine_part + ROWS * D + ROWS + row, sum);
           }
         }
       }
-      if (r < rows && p.lse)
-        p.lse[static_cast<long long>(hq) * p.kv.M + token] = sum > 0.f ? (top + log2f(sum)) * k8::kLn2 : -INFINITY;
+      if (!whole && ok) {   // the 8 warps together: the last block to arrive adds the parts
+        __threadfence();
+        ok = join();
+        if (threadIdx.x == 128)
+          ctrl->last = ok && atom_add_acq_rel_gpu(p.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+        ok = ok && join();
+        if (ok && ctrl->last) {
+          __threadfence();
+          if (r < rows) {
+            top = -INFINITY;
+            for (int k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(slot_of(k) + ROWS * D + row));
+            sum = 0.f;
+            for (int k = c0; k <= c1; ++k)
+              sum += (top == -INFINITY ? 0.f : k8::ex2(__ldcg(slot_of(k) + ROWS * D + row) - top)) *
+                     __ldcg(slot_of(k) + ROWS * D + ROWS + row);
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += 16) {
+              float acc[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+              for (int k = c0; k <= c1; ++k) {
+                const float f = top == -INFINITY ? 0.f : k8::ex2(__ldcg(slot_of(k) + ROWS * D + row) - top);
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                  const float4 y = __ldcg(reinterpret_cast<const float4*>(slot_of(k)) + ((d0 + e) >> 2) * ROWS + row);
+                  acc[e] = fmaf(f, y.x, acc[e]);
+                  acc[e + 1] = fmaf(f, y.y, acc[e + 1]);
+                  acc[e + 2] = fmaf(f, y.z, acc[e + 2]);
+                  acc[e + 3] = fmaf(f, y.w, acc[e + 3]);
+                }
+              }
+              put(d0, acc, sum > 0.f ? 1.f / sum : 0.f);
+            }
+            put_lse();
+          }
+          if (threadIdx.x == 128) p.counters[c0] = 0;
+        }
+      }
+      release();
     }
   }
 
@@ -462,6 +827,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0 && *abortf)   // after an abort nobody has waited for the copies in flight
     for (int s = 0; s < C::STAGES; ++s)
       if (ctrl->armed & (1u << s)) k8::drain_wait(&ctrl->full[s], (ctrl->armed_parity >> s) & 1);
+  if (threadIdx.x == 0 && atomicAdd(prm.claim + 1, 1u) == gridDim.x - 1) prm.claim[0] = prm.claim[1] = 0;   // the last block
 }
 
 }  // namespace k9
