@@ -500,3 +500,18 @@ def test_a_wait_that_runs_out_is_reported(cuda_device):
         h.check()
     _check_attention(h, c, [300, 200], 4)
     h.close()
+
+
+def test_prompts_of_many_sequences(handle):
+    """More sequences than threads of a block, lengths of many kinds, some empty: the plan
+    of the tensor-core form; then few tiles of long keys, shared by many blocks."""
+    g = np.random.default_rng(60)
+    new = [int(x) for x in g.integers(0, 9, 900)]
+    lens = [n + int(x) for n, x in zip(new, g.integers(0, 40, 900))]
+    lens = [max(n, 1) for n in lens]
+    new[17], lens[17] = 300, 350
+    c = Cache("bf16", lens, 1, 64, 16, seed=61)
+    assert "tensor" in _check_attention(handle, c, new, 3)
+    c = Cache("bf16", [6000, 50, 2900], 2, 128, 128, seed=62)
+    _check_attention(handle, c, [20, 30, 0], 8)
+    _check_attention(handle, c, [40, 1, 70], 8, window=1500, sinks=200)

@@ -14,9 +14,10 @@
 // One block per SM takes row tiles (key head by key head, the longest of a sequence
 // first) from a counter, so that at any time the blocks read the keys and values of
 // few heads, close together: the copies' way through L2 is what a scattered order
-// loses on (ragged prompts ran 1.8 times longer with the heads side by side). Whole
-// tiles only fill whole waves; the (row tile, key tile) units of the rest, or of all
-// when there are fewer tiles than SMs, are dealt evenly over the blocks. A block's
+// loses on (ragged prompts ran 1.8 times longer with the heads side by side). Where
+// the tiles are long, whole ones only fill whole waves, and the (row tile, key tile)
+// units of the rest, or of all when there are fewer tiles than SMs, are dealt evenly
+// over the blocks. A block's
 // first and last pieces of those may be parts: they leave fp32 partial sums, and the
 // last block to arrive adds them in block order. Which block takes a whole tile does
 // not touch its result, and the parts are cut by block number, so results do not
@@ -25,17 +26,21 @@
 // Roles (12 warps): 0 takes pieces of work, announces them to the others through a
 // two-entry queue and copies K and V tiles by TMA, page by page, into a ring;
 // 1 issues the products; 2 and 3 fetch the next piece's Q; 4-7 and 8-11 are the two
-// sub-tiles' softmax, which also write the result. The first half of a tile's
-// probabilities is handed to the second product while the other half is computed.
+// sub-tiles' softmax, which also write the result.
 // A row's accumulators are rescaled only when its maximum has grown by more than 8
 // (a factor of 256) since the last time: the probabilities stay below 256, exact
 // enough in bf16's and fp32's floating formats, and most key tiles need no pass
 // over O.
 //
 // Bound: a key tile costs 4 * 128 * 128 * D multiply-adds on the tensor pipe (2048
-// cycles at D = 128) and 2 * 128 * 128 exponentials, 2048 cycles on the
-// special-function units alone; so a part of them is computed on the FMA pipe
-// (exp2_fma).
+// cycles at D = 128) and 2 * 128 * 128 exponentials (2048 cycles of the special-
+// function units, which run under the products). What keeps it from the tensor peak
+// is the way from a sub-tile's scores to its probabilities (about 2100 cycles: 80 to
+// load a row, 450 for its maximum, 1500 for the exponentials) being longer than the
+// other sub-tile's products (1350: Q K^T reads both operands from shared memory, at
+// its full rate). Measured and left out: a part of the exponentials as polynomials on
+// the FMA pipe (1345 -> 1369 .. 1564 us with one pair in eight .. two), and the first
+// half of a tile's probabilities handed over early (1345 -> 1401 us).
 //
 // Slots that no row of the piece sees are not copied (whole pages) or are zeroed
 // in V's tile before the product (rows), since 0 * NaN would reach the result;
@@ -54,15 +59,38 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem desc]: A is bf16, two consecutive k packed in a
-// 32-bit column, row = lane.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// The products are issued from convergent code under a predicate (`issue`, one lane)
+// rather than inside a branch: the descriptors then stay in uniform registers and an
+// instruction costs the issuing warp a few cycles instead of the ~90 that kept 64-cycle
+// products waiting.
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, bf16, fp32 accumulate.
+__device__ __forceinline__ void umma_bf16_if(uint32_t issue, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issue)
+      : "memory");
+}
+// The same with A in TMEM: bf16, two consecutive k packed in a 32-bit column, row = lane.
+__device__ __forceinline__ void umma_bf16_ts_if(uint32_t issue, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t issue, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(issue)
       : "memory");
 }
 // Operand whose rows (128 bytes = 64 values of the M or N dimension, 128-byte
@@ -104,26 +132,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer (added to
-// 1.5 * 2^23 it sits in the low bits) and |f| <= 1/2, 2^f by the polynomial of degree
-// 4 whose largest relative error is least (Remez exchange: 2.6e-6), n added to the
-// exponent. x is held at -126 from below (the result is then 2^-126 or less).
-__device__ __forceinline__ f32x2 exp2_fma(f32x2 x) {
-  float a, b;
-  unpk2(x, a, b);
-  x = pk2(fmaxf(a, -126.f), fmaxf(b, -126.f));
-  const f32x2 magic = pk2(12582912.f, 12582912.f);
-  const f32x2 t = add2(x, magic);
-  const f32x2 f = sub2(x, sub2(t, magic));
-  f32x2 y = fma2(f, pk2(0.00957010221f, 0.00957010221f), pk2(0.0559178591f, 0.0559178591f));
-  y = fma2(f, y, pk2(0.240247443f, 0.240247443f));
-  y = fma2(f, y, pk2(0.693121791f, 0.693121791f));
-  y = fma2(f, y, pk2(0.999999285f, 0.999999285f));
-  float t0, t1, y0, y1;
-  unpk2(t, t0, t1);
-  unpk2(y, y0, y1);
-  return pk2(__int_as_float(__float_as_int(y0) + (__float_as_int(t0) << 23)),
-             __int_as_float(__float_as_int(y1) + (__float_as_int(t1) << 23)));
+// Bits 0 .. n set (none for n < 0, all from 31 on).
+__device__ __forceinline__ uint32_t ones_to(int n) {
+  return n < 0 ? 0u : 0xffffffffu >> (31 - min(n, 31));
 }
 
 namespace k9 {
@@ -135,8 +146,7 @@ constexpr int ROWS = 2 * TILE;
 constexpr int REG_SOFTMAX = 208, REG_OTHER = 80;   // 256 * 208 + 128 * 80 <= 384 * 168, the launch's registers
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float GROWTH = 8.f;          // rescale when the maximum (base 2) has grown by more
-constexpr int FMA_EVERY = 0;           // one pair of exponentials in so many goes to the FMA pipe (0: none)
-constexpr int kMaxSeqs = 32768;        // the plan's prefix sums fit the ring
+constexpr int kMaxSeqs = 16384;        // the plan's two prefix sums fit the ring
 constexpr int CTRL_BYTES = 2048;
 constexpr int kPartFloats = ROWS * (128 + 2);   // of one slot: accumulators, maximum, sum
 
@@ -148,7 +158,7 @@ struct Cfg {
   static constexpr int STAGES = D == 128 ? 5 : 10;
   static constexpr int SMEM = 2 * TILE_BYTES + STAGES * TILE_BYTES + 1024 + CTRL_BYTES;
   static constexpr uint32_t S0 = 0, O0 = 256;       // TMEM columns: S at 0 and 128 (P over it), O at 256 and 256 + D
-  static_assert((kMaxSeqs + 1) * 4 <= STAGES * TILE_BYTES, "prefix sums in the ring");
+  static_assert(2 * (kMaxSeqs + 1) * 4 <= STAGES * TILE_BYTES, "prefix sums in the ring");
 };
 
 struct Params {
@@ -208,7 +218,7 @@ struct Piece {
 };
 
 struct Ctrl {
-  uint64_t full[10], empty[10], s_full[2], p_half[2][2], o_full[2], q_full, q_empty, work_full[2], work_empty[2], join, drain;
+  uint64_t full[10], empty[10], s_full[2], p_full[2], o_full[2], q_full, q_empty, work_full[2], work_empty[2], join, drain;
   uint32_t tmem_base;
   uint32_t armed, armed_parity;   // ring slots with a copy issued, and the parity of each one's last
   int abort_flag;
@@ -218,6 +228,22 @@ struct Ctrl {
   Piece piece[2];
 };
 static_assert(sizeof(Ctrl) <= CTRL_BYTES, "the control block");
+
+// Sequence and row tile of tile `idx` of the plan's order, from the prefix sums: all
+// row tiles, and late ones, before each sequence.
+__device__ __forceinline__ void tile_at(const int* all, const int* late, int B, long long N1, long long idx, int& b, int& j) {
+  const bool second = idx >= N1;
+  auto before = [&](int i) { return second ? late[i] : all[i] - late[i]; };
+  const int r = static_cast<int>((second ? idx - N1 : idx) % before(B));
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {   // the last sequence whose first tile of the kind is at most r
+    const int mid = (lo + hi + 1) >> 1;
+    if (before(mid) <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  b = lo;
+  j = (second ? late[lo + 1] - late[lo] : all[lo + 1] - all[lo]) - 1 - (r - before(lo));
+}
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -240,8 +266,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctrl->s_full[s], 1);
-      mbar_init(&ctrl->p_half[s][0], 4);
-      mbar_init(&ctrl->p_half[s][1], 4);
+      mbar_init(&ctrl->p_full[s], 4);
       mbar_init(&ctrl->o_full[s], 1);
     }
     mbar_init(&ctrl->q_full, 2);
@@ -289,29 +314,41 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (threadIdx.x == 0) first_tile[0] = 0;
   __syncthreads();
-  auto seq_of = [&](int r) {   // sequence of row tile r: the last whose first row tile is at most r
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (first_tile[mid] <= r) lo = mid;
-      else hi = mid - 1;
-    }
-    return lo;
-  };
-  // tiles: N = Hkv R in the order (head, sequence, row tile from the last down). The
-  // first W, whole waves of them, are taken whole; the rest are shared.
-  const long long N = static_cast<long long>(R) * p.kv.Hkv;
+  // Tiles in the order they are taken: first, key head by key head and from the longest
+  // of a sequence down, those behind a sequence's first `cut` row tiles; then these
+  // first ones, key head by key head, about two for every block: causal tiles grow from
+  // a sequence's start, so the blocks end on short ones.
   const int G = gridDim.x;
-  const long long W = N / G * G;
-  const int rest = static_cast<int>(N - W);   // < G <= THREADS
-  int units_rest, my_tiles = 0;
-  if (static_cast<int>(threadIdx.x) < rest) {
-    const int r = static_cast<int>((W + threadIdx.x) % R), b = seq_of(r);
-    my_tiles = row_tile(p, b, first_tile[b + 1] - 1 - r).tiles();   // (r counts down inside a sequence)
+  const int cut = static_cast<int>((2LL * G + static_cast<long long>(p.kv.Hkv) * B - 1) / (static_cast<long long>(p.kv.Hkv) * B));
+  int late = 0;   // row tiles (of one key head) of the second kind
+  int* late_tile = first_tile + kMaxSeqs + 1;
+  for (int i = 0; i < B; i += THREADS) {
+    const int b = i + threadIdx.x;
+    int total;
+    const int x = block_scan(b < B ? min(first_tile[b + 1] - first_tile[b], cut) : 0, total);
+    if (b < B) late_tile[b + 1] = late + x;
+    late += total;
+  }
+  if (threadIdx.x == 0) late_tile[0] = 0;
+  __syncthreads();
+  const int early = R - late;
+  const long long N = static_cast<long long>(R) * p.kv.Hkv, N1 = static_cast<long long>(early) * p.kv.Hkv;
+  // Whole waves of tiles are taken whole. The rest are shared, where a share is eight
+  // key tiles at least (a part costs its sums' way through memory, about 15 us) and
+  // there are fewer tiles than blocks, or the shares are worth more than a last wave.
+  const long long full = N / G * G;
+  int units_rest = 0, my_tiles = 0;
+  const int rest0 = static_cast<int>(N - full);   // < G <= THREADS
+  if (static_cast<int>(threadIdx.x) < rest0) {
+    int b, j;
+    tile_at(first_tile, late_tile, B, N1, full + threadIdx.x, b, j);
+    my_tiles = row_tile(p, b, j).tiles();
   }
   const int my_end = block_scan(my_tiles, units_rest);
-  // at least four key tiles a block, unless there are more tiles than that makes blocks
-  const int Gr = rest == 0 ? 0 : min(G, max(rest, units_rest / 4));
+  const bool share_rest = full == 0 || units_rest >= 8 * G;
+  const long long W = share_rest ? full : N;
+  const int rest = share_rest ? rest0 : 0;
+  const int Gr = rest == 0 ? 0 : min(G, max(rest, units_rest / 8));
   const bool shares = static_cast<int>(blockIdx.x) < Gr;
   const int u0 = shares ? static_cast<int>(static_cast<long long>(blockIdx.x) * units_rest / Gr) : 0;
   const int u1 = shares ? static_cast<int>(static_cast<long long>(blockIdx.x + 1) * units_rest / Gr) : 0;
@@ -355,15 +392,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool withhold = prm.stall != 0 && blockIdx.x == 0;
     bool ok = true;
     uint32_t sent = 0;
-    int at_head = 0, at_b = 0, at_r = 0;   // the last tile taken: its head and sequence, row tiles before that sequence
+    // the last tile taken: its kind, head and sequence, row tiles of that kind before the sequence
+    int at_kind = 0, at_head = 0, at_b = 0, at_r = 0;
     // Tile `idx` for the whole warp: 32 sequences at a time from the last one on.
     auto find = [&](long long idx, int& head, int& b, int& j) {
-      head = static_cast<int>(idx / R);
-      const int r = static_cast<int>(idx - static_cast<long long>(head) * R);
-      if (head != at_head || r < at_r) at_b = at_r = 0;
+      const int kind = idx >= N1;
+      const int per = kind ? late : early;
+      if (kind) idx -= N1;
+      head = static_cast<int>(idx / per);
+      const int r = static_cast<int>(idx - static_cast<long long>(head) * per);
+      if (kind != at_kind || head != at_head || r < at_r) at_b = at_r = 0;
+      at_kind = kind;
       at_head = head;
       while (at_b < B) {
-        const int mine = at_b + lane < B ? row_tiles(p, at_b + lane) : 0;
+        const int all = at_b + lane < B ? row_tiles(p, at_b + lane) : 0;
+        const int mine = kind ? min(all, cut) : max(all - cut, 0);
         int x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -373,11 +416,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         const unsigned behind = __ballot_sync(0xffffffffu, at_r + x > r);
         if (behind) {
           const int l = __ffs(behind) - 1;
-          const int end = at_r + __shfl_sync(0xffffffffu, x, l), n = __shfl_sync(0xffffffffu, mine, l);
+          const int end = at_r + __shfl_sync(0xffffffffu, x, l), m = __shfl_sync(0xffffffffu, mine, l);
+          const int n = __shfl_sync(0xffffffffu, all, l);
           at_b += l;
-          at_r = end - n;
+          at_r = end - m;
           b = at_b;
-          j = end - 1 - r;
+          j = (kind ? m : n) - 1 - (r - at_r);
           return;
         }
         at_r += __shfl_sync(0xffffffffu, x, 31);
@@ -474,31 +518,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     // descriptors differ in their address field alone (16-byte units)
     const uint64_t kmajor = sw128_desc(0), nmajor = sw128_mn_desc(0, C::HALF_BYTES);
     const uint32_t q16 = smem_u32(smem) >> 4, ring16 = smem_u32(ring) >> 4;
+    const uint32_t one = lane == 0;
+    auto commit = [&](uint64_t* bar) { umma_commit_if(one, bar); };
     auto qk = [&](int s, int at) {
-      if (lane == 0) {
-        const uint64_t q = kmajor + q16 + s * (C::TILE_BYTES >> 4), k = kmajor + ring16 + at * (C::TILE_BYTES >> 4);
+      const uint64_t q = kmajor + q16 + s * (C::TILE_BYTES >> 4), k = kmajor + ring16 + at * (C::TILE_BYTES >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = ((kk >> 2) * C::HALF_BYTES + (kk & 3) * 32) >> 4;
-          umma_bf16(tmem + C::S0 + s * TILE, q + o, k + o, idesc_qk, kk > 0);
-        }
-        umma_commit(&ctrl->s_full[s]);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = ((kk >> 2) * C::HALF_BYTES + (kk & 3) * 32) >> 4;
+        umma_bf16_if(one, tmem + C::S0 + s * TILE, q + o, k + o, idesc_qk, kk > 0);
       }
-      __syncwarp();
+      commit(&ctrl->s_full[s]);
     };
-    auto pv = [&](int s, int at, int h, bool first) {   // half h of the keys
-      if (lane == 0) {
-        const uint64_t v = nmajor + ring16 + at * (C::TILE_BYTES >> 4) + h * (TILE / 2 * 128 >> 4);
-        const uint32_t o = tmem + C::O0 + s * D, a = tmem + C::S0 + s * TILE + h * (TILE / 4);
+    auto pv = [&](int s, int at, bool first) {
+      const uint64_t v = nmajor + ring16 + at * (C::TILE_BYTES >> 4);
+      const uint32_t o = tmem + C::O0 + s * D, a = tmem + C::S0 + s * TILE;
 #pragma unroll
-        for (int kk = 0; kk < TILE / 32; ++kk)
-          umma_bf16_ts(o, a + kk * 8, v + kk * (2048 >> 4), idesc_pv, !first || h > 0 || kk > 0);
-      }
-      __syncwarp();
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (lane == 0) umma_commit(bar);
-      __syncwarp();
+      for (int kk = 0; kk < TILE / 16; ++kk)
+        umma_bf16_ts_if(one, o, a + kk * 8, v + kk * (2048 >> 4), idesc_pv, !first || kk > 0);
     };
     auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
       const bool r = warp_wait(bar, parity & 1u, abortf, status, code, p.wait_ns);
@@ -538,27 +574,19 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
         }
         advance();
+        // (K first: nothing is waited for between a sub-tile's two products)
         const int ks = slot;
-        bool have_k = false;
+        if (i + 1 < t1) ok = wait(&ctrl->full[ks], ph, kStatusWaitFull);
         for (int s = 0; s < 2 && ok; ++s) {
           if (i < reach[s]) {
-            for (int h = 0; h < 2 && ok; ++h) {
-              ok = wait(&ctrl->p_half[s][h], done[s], kStatusWaitConv);
-              if (ok) pv(s, vs, h, i == t0);
-            }
+            ok = wait(&ctrl->p_full[s], done[s], kStatusWaitConv);
             if (!ok) break;
             ++done[s];
-            if (i + 1 == min(t1, reach[s])) commit(&ctrl->o_full[s]);
+            pv(s, vs, i == t0);
+            if (i + 1 < t1 && i + 1 < reach[s]) qk(s, ks);
+            else commit(&ctrl->o_full[s]);
           }
           if (s == 1) commit(&ctrl->empty[vs]);
-          if (i + 1 < t1 && i + 1 < reach[s]) {
-            if (!have_k) {
-              ok = wait(&ctrl->full[ks], ph, kStatusWaitFull);
-              if (!ok) break;
-              have_k = true;
-            }
-            qk(s, ks);
-          }
         }
         if (ok && i + 1 < t1) {
           commit(&ctrl->empty[ks]);
@@ -588,21 +616,28 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (pieces > 0) ok = warp_wait(&ctrl->q_empty, (pieces - 1) & 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
       if (!ok) break;
       ++pieces;
-      int row = t / CH;
-      int token = first + (r0 + row) / p.group, hq = (r0 + row) % p.group;
-      const int dt = STEP / p.group, dh = STEP % p.group;
-#pragma unroll 4
-      for (; row < ROWS; row += STEP) {
-        const bool in = r0 + row < rows;
-        const bf16* src = in ? p.q + (static_cast<long long>(head0 + hq) * p.kv.M + token) * D + c * 8 : p.q;
-        k8::cp16(smem_u32(smem) + (row / TILE) * C::TILE_BYTES + (c >> 3) * C::HALF_BYTES + (row % TILE) * 128 +
-                     (((c & 7) ^ (row & 7)) << 4),
-                 src, in ? 16 : 0);
-        token += dt;
-        hq += dh;
-        if (hq >= p.group) {
-          hq -= p.group;
-          ++token;
+      // rows t / CH, + STEP, ..: the row's token and head advance without divisions, and
+      // the swizzle repeats every 8 rows
+      const int row0 = t / CH;
+      int hq = (r0 + row0) % p.group;
+      const bf16* src = p.q + (static_cast<long long>(head0 + hq) * p.kv.M + first + (r0 + row0) / p.group) * D + c * 8;
+      const long long step = (static_cast<long long>(STEP % p.group) * p.kv.M + STEP / p.group) * D;
+      const long long wrap = (1 - static_cast<long long>(p.group) * p.kv.M) * D;
+      const uint32_t dst = smem_u32(smem) + (c >> 3) * C::HALF_BYTES;
+#pragma unroll 2
+      for (int k = 0; k < ROWS / 8; ++k) {
+#pragma unroll
+        for (int e = 0; e < 8 / STEP; ++e) {
+          const int row = k * 8 + e * STEP + row0;
+          const bool in = r0 + row < rows;
+          k8::cp16(dst + (row >= TILE ? C::TILE_BYTES - TILE * 128 : 0) + row * 128 + (((c & 7) ^ ((e * STEP + row0) & 7)) << 4),
+                   in ? src : p.q, in ? 16 : 0);
+          src += step;
+          hq += STEP % p.group;
+          if (hq >= p.group) {
+            hq -= p.group;
+            src += wrap;
+          }
         }
       }
       k8::cp_commit();
@@ -651,10 +686,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
         // some row of the warp does not see some key
         if (key + TILE - 1 > w0 || (p.window > 0 && key <= w1 - p.window && key + TILE > p.sinks)) {
-          const int hi = pos - key, wlo = p.window > 0 ? hi - p.window + 1 : -(1 << 30), sk = p.sinks - key;
+          const int hi = pos - key, lo = p.window > 0 ? hi - p.window : -1, sk = p.sinks - key;
 #pragma unroll
-          for (int c = 0; c < TILE; ++c)
-            if (!(c <= hi && (c >= wlo || c < sk))) x[c] = 0xff800000u;   // -inf
+          for (int c0 = 0; c0 < TILE; c0 += 32) {   // bit c: key c0 + c is seen (at most hi; above lo, or below sk)
+            const uint32_t seen = ones_to(hi - c0) & (~ones_to(lo - c0) | ones_to(sk - 1 - c0));
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(seen >> c & 1u)) x[c0 + c] = 0xff800000u;   // -inf
+          }
         }
         float m4[4];
 #pragma unroll
@@ -693,28 +732,21 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int c = 0; c < 16; ++c) {
             f32x2 y = fma2(pk2(__uint_as_float(x[h * 32 + 2 * c]), __uint_as_float(x[h * 32 + 2 * c + 1])), scale2, base2);
             float a, d;
-            if (FMA_EVERY > 0 && c % (FMA_EVERY > 0 ? FMA_EVERY : 1) == FMA_EVERY - 1) {
-              y = exp2_fma(y);
-              unpk2(y, a, d);
-            } else {
-              unpk2(y, a, d);
-              a = k8::ex2(a);
-              d = k8::ex2(d);
-              y = pk2(a, d);
-            }
+            unpk2(y, a, d);
+            a = k8::ex2(a);
+            d = k8::ex2(d);
+            y = pk2(a, d);
             if (c & 1) part2 = add2(part2, y);
             else sum2 = add2(sum2, y);
             w[c] = pack_bf16x2(a, d);
           }
           tmem_st16(ts + h * 16, w);
-          if (h & 1) {   // half the tile's probabilities are in place
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctrl->p_half[s][h >> 1]);
-          }
         }
         sum2 = add2(sum2, part2);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->p_full[s]);
       }
       // ---- the piece's result
       float a, c;
