@@ -27,7 +27,6 @@
 #include "k5_tp.cuh"
 #include "k7_kv.cuh"
 #include "k8_attend.cuh"
-#include "k8_rows.cuh"
 #include "k9_prompt.cuh"
 
 using fnl::bf16;
@@ -1552,18 +1551,23 @@ fnl_status page_map(fnl_handle* h, CUtensorMap* m, const KvParams& kv, const voi
   return FNL_OK;
 }
 
-template <int D>
+template <int D, int FMT>
 fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a) {
   using namespace fnl::k9;
   fnl_status st = get_encoder(h);
   if (st != FNL_OK) return st;
   CUtensorMap mk, mv;
-  if ((st = page_map(h, &mk, a.kv, a.kv.k, D)) != FNL_OK || (st = page_map(h, &mv, a.kv, a.kv.v, D)) != FNL_OK) return st;
-  if ((st = set_smem(h, k9_prompt<D>, Cfg<D>::SMEM)) != FNL_OK) return st;
+  if (FMT == fnl::kKvBf16) {   // 4-bit pages are not copied by tensor maps
+    if ((st = page_map(h, &mk, a.kv, a.kv.k, D)) != FNL_OK || (st = page_map(h, &mv, a.kv, a.kv.v, D)) != FNL_OK) return st;
+  } else {
+    memset(&mk, 0, sizeof(mk));
+    memset(&mv, 0, sizeof(mv));
+  }
+  if ((st = set_smem(h, k9_prompt<D, FMT>, Cfg<D, FMT>::SMEM)) != FNL_OK) return st;
   // the warps' register shares must fit what the block is launched with, or its warps would wait for them forever
   static const int regs = [] {
     cudaFuncAttributes fa{};
-    return cudaFuncGetAttributes(&fa, k9_prompt<D>) == cudaSuccess ? fa.numRegs : 0;
+    return cudaFuncGetAttributes(&fa, k9_prompt<D, FMT>) == cudaSuccess ? fa.numRegs : 0;
   }();
   if (regs * THREADS < 256 * REG_SOFTMAX + 128 * REG_OTHER)
     return fail(h, FNL_ERR_UNSUPPORTED, "the paged attention kernel was built with %d registers a thread", regs);
@@ -1581,14 +1585,14 @@ fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(h->num_sms));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = Cfg<D>::SMEM;
+  cfg.dynamicSmemBytes = Cfg<D, FMT>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k9_prompt<D>, mk, mv, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k9_prompt<D, FMT>, mk, mv, p);
   if (e != cudaSuccess) return cuda_fail(h, e, "launch of the paged attention kernel");
   return FNL_OK;
 }
@@ -1606,18 +1610,10 @@ fnl_status split_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p)
 
 template <int D, int FMT>
 fnl_status attend_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p) {
-  char buf[160];
   const long long rows = static_cast<long long>(p.kv.max_q) * p.group;
   if (rows <= 8) return split_launch<D, FMT, 1>(h, s, p);
   if (rows <= 16) return split_launch<D, FMT, 2>(h, s, p);
-  if (FMT == fnl::kKvBf16) return prompt_launch<D>(h, s, p);
-  typedef fnl::k8::RowsCfg<D, FMT> C;
-  const long long tiles = (static_cast<long long>(p.kv.max_q) * p.group + C::ROWS - 1) / C::ROWS;
-  if (tiles > 0x7fffffffLL) return fail(h, FNL_ERR_UNSUPPORTED, "max_q * Hq / Hkv is too large");
-  snprintf(buf, sizeof(buf), "paged attention, row form, grid %lld x %d x %d", tiles, p.kv.Hkv, p.kv.B);
-  h->plan_text = buf;
-  return kv_launch(h, fnl::k8::k8_attend_rows<D, FMT>, dim3(static_cast<unsigned>(tiles), p.kv.Hkv, p.kv.B), C::THREADS,
-                   C::SMEM, s, p);
+  return prompt_launch<D, FMT>(h, s, p);
 }
 
 }  // namespace

@@ -42,6 +42,12 @@
 // the FMA pipe (1345 -> 1369 .. 1564 us with one pair in eight .. two), and the first
 // half of a tile's probabilities handed over early (1345 -> 1401 us).
 //
+// 4-bit pages: the copying warp only deals out the pieces; warps 2 and 3 unpack key and
+// value tiles as code - 8, which bf16 holds exactly, and put the rows' scales beside
+// them. The softmax applies them in fp32: s (q . (c - 8)) + (m + 8 s) sum(q) to the
+// scores, p s as the second product's operand and sum(p (m + 8 s)) added at the end,
+// as K8 does; neither keys nor values are rounded.
+//
 // Slots that no row of the piece sees are not copied (whole pages) or are zeroed
 // in V's tile before the product (rows), since 0 * NaN would reach the result;
 // their scores are replaced, not added to.
@@ -143,22 +149,27 @@ constexpr int WARPS = 12;
 constexpr int THREADS = WARPS * 32;
 constexpr int TILE = 128;              // keys of a tile, rows of a sub-tile
 constexpr int ROWS = 2 * TILE;
-constexpr int REG_SOFTMAX = 208, REG_OTHER = 80;   // 256 * 208 + 128 * 80 <= 384 * 168, the launch's registers
+constexpr int REG_SOFTMAX = 200, REG_OTHER = 96;   // 256 * 200 + 128 * 96 <= 384 * 168, the launch's registers
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float GROWTH = 8.f;          // rescale when the maximum (base 2) has grown by more
 constexpr int kMaxSeqs = 16384;        // the plan's two prefix sums fit the ring
 constexpr int CTRL_BYTES = 2048;
 constexpr int kPartFloats = ROWS * (128 + 2);   // of one slot: accumulators, maximum, sum
 
-template <int D>
+template <int D, int FMT>
 struct Cfg {
+  static constexpr bool INT4 = FMT == kKvInt4;
   static constexpr int HALVES = D / 64;
   static constexpr int TILE_BYTES = TILE * D * 2;   // Q sub-tile, K tile, V tile: HALVES blocks of 128 x 64
   static constexpr int HALF_BYTES = TILE * 128;
-  static constexpr int STAGES = D == 128 ? 5 : 10;
-  static constexpr int SMEM = 2 * TILE_BYTES + STAGES * TILE_BYTES + 1024 + CTRL_BYTES;
+  static constexpr int STAGES = (INT4 ? 4 : 5) * (D == 128 ? 1 : 2);
+  // 4-bit pages: scales of a tile's keys, then of its values, four tiles deep: for keys
+  // c, c + 1 the four floats (scale, scale, offset, offset)
+  static constexpr int AFFINE_TILE = 2 * TILE * 8, AFFINES = 4;
+  static constexpr int AFFINE = INT4 ? AFFINES * AFFINE_TILE : 0;
+  static constexpr int SMEM = 2 * TILE_BYTES + STAGES * TILE_BYTES + AFFINE + 1024 + CTRL_BYTES;
   static constexpr uint32_t S0 = 0, O0 = 256;       // TMEM columns: S at 0 and 128 (P over it), O at 256 and 256 + D
-  static_assert(2 * (kMaxSeqs + 1) * 4 <= STAGES * TILE_BYTES, "prefix sums in the ring");
+  static_assert(2 * (kMaxSeqs + 1) * 4 <= STAGES * TILE_BYTES + AFFINE, "prefix sums in the ring");
 };
 
 struct Params {
@@ -175,7 +186,6 @@ struct RowTile {
   int lo_tile, sink_tiles, n0, n1; // key tiles that the two sub-tiles reach: the first n0, n1 of the list
   k8::Sight sight;
   __device__ __forceinline__ int tiles() const { return max(max(n0, n1), 1); }   // one at least writes the rows
-  __device__ __forceinline__ int key_of(int i) const { return (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE; }
 };
 __device__ __forceinline__ RowTile row_tile(const AttnParams& p, int b, int j) {
   const KvSeq q = kv_seq(p.kv, b);
@@ -213,12 +223,13 @@ __device__ __forceinline__ int row_tiles(const AttnParams& p, int b) {
 // Parts of a tile shared by the blocks c0 .. c1.
 struct Piece {
   RowTile t;
-  int head, t0, t1, c0, c1;
+  int head, b, t0, t1, c0, c1;
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == t.tiles(); }
 };
 
 struct Ctrl {
   uint64_t full[10], empty[10], s_full[2], p_full[2], o_full[2], q_full, q_empty, work_full[2], work_empty[2], join, drain;
+  uint64_t a_full[4], a_empty[4];
   uint32_t tmem_base;
   uint32_t armed, armed_parity;   // ring slots with a copy issued, and the parity of each one's last
   int abort_flag;
@@ -245,29 +256,34 @@ __device__ __forceinline__ void tile_at(const int* all, const int* late, int B, 
   j = (second ? late[lo + 1] - late[lo] : all[lo + 1] - all[lo]) - 1 - (r - before(lo));
 }
 
-template <int D>
+template <int D, int FMT>
 __global__ void __launch_bounds__(THREADS, 1)
     k9_prompt(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
               const __grid_constant__ Params prm) {
-  typedef Cfg<D> C;
+  typedef Cfg<D, FMT> C;
   const AttnParams& p = prm.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + 2 * C::TILE_BYTES;
-  Ctrl* ctrl = reinterpret_cast<Ctrl*>(ring + C::STAGES * C::TILE_BYTES);
+  uint8_t* affine = ring + C::STAGES * C::TILE_BYTES;
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(affine + C::AFFINE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abortf = &ctrl->abort_flag;
   int* status = p.kv.status;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->full[s], C::INT4 ? 2 : 1);   // the unpacking warps, or the TMA copies
       mbar_init(&ctrl->empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctrl->s_full[s], 1);
       mbar_init(&ctrl->p_full[s], 4);
       mbar_init(&ctrl->o_full[s], 1);
+    }
+    for (int s = 0; s < C::AFFINES; ++s) {
+      mbar_init(&ctrl->a_full[s], 2);
+      mbar_init(&ctrl->a_empty[s], 8);
     }
     mbar_init(&ctrl->q_full, 2);
     mbar_init(&ctrl->q_empty, 1);
@@ -333,9 +349,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   const int early = R - late;
   const long long N = static_cast<long long>(R) * p.kv.Hkv, N1 = static_cast<long long>(early) * p.kv.Hkv;
-  // Whole waves of tiles are taken whole. The rest are shared, where a share is eight
-  // key tiles at least (a part costs its sums' way through memory, about 15 us) and
-  // there are fewer tiles than blocks, or the shares are worth more than a last wave.
+  // Whole waves of tiles are taken whole. The rest are shared in parts of six key tiles
+  // at least (a part costs its sums' way through memory, about 15 us, six key tiles'
+  // time), where there are fewer tiles than blocks or where that ends sooner than
+  // another wave, the longest of the rest.
   const long long full = N / G * G;
   int units_rest = 0, my_tiles = 0;
   const int rest0 = static_cast<int>(N - full);   // < G <= THREADS
@@ -344,11 +361,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     tile_at(first_tile, late_tile, B, N1, full + threadIdx.x, b, j);
     my_tiles = row_tile(p, b, j).tiles();
   }
+  if (threadIdx.x == 0) ctrl->last = 0;
   const int my_end = block_scan(my_tiles, units_rest);
-  const bool share_rest = full == 0 || units_rest >= 8 * G;
+  const int longest_in_warp = __reduce_max_sync(0xffffffffu, my_tiles);
+  if (lane == 0 && longest_in_warp > 0) atomicMax(&ctrl->last, longest_in_warp);
+  __syncthreads();
+  const bool share_rest = full == 0 || units_rest / G + 6 < ctrl->last;
   const long long W = share_rest ? full : N;
   const int rest = share_rest ? rest0 : 0;
-  const int Gr = rest == 0 ? 0 : min(G, max(rest, units_rest / 8));
+  const int Gr = rest == 0 ? 0 : min(G, max(rest, units_rest / 6));
   const bool shares = static_cast<int>(blockIdx.x) < Gr;
   const int u0 = shares ? static_cast<int>(static_cast<long long>(blockIdx.x) * units_rest / Gr) : 0;
   const int u1 = shares ? static_cast<int>(static_cast<long long>(blockIdx.x + 1) * units_rest / Gr) : 0;
@@ -438,6 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) {
         if (t1 != 0) w.t = row_tile(p, b, j);
         w.head = head;
+        w.b = b;
         w.t0 = t0;
         w.t1 = t1 < 0 ? w.t.tiles() : t1;
         w.c0 = c0;
@@ -446,6 +468,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
       ++sent;
+      if (C::INT4) return;   // 4-bit tiles: warps 2 and 3
       t1 = w.t1;
       const k8::Sight sight = w.t.sight;
       const int lo_tile = w.t.lo_tile, sink_tiles = w.t.sink_tiles;
@@ -563,7 +586,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = wait(&ctrl->full[slot], ph, kStatusWaitFull);
         if (!ok) break;
         const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
-        if (key + TILE > sight.len || (key < sight.lo && key + TILE > sight.sinks)) {
+        if (!C::INT4 && (key + TILE > sight.len || (key < sight.lo && key + TILE > sight.sinks))) {
           // rows of V that nobody sees become zeros (a warp instruction covers 4 rows' halves)
           for (int r = lane >> 3; r < TILE; r += 4)
             if (!sight.any(key + r))
@@ -605,12 +628,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_OTHER));
     constexpr int CH = D / 8, STEP = 64 / CH;   // 16-byte chunks of a row; rows of one turn of the 64 threads
     const int t = threadIdx.x - 64, c = t % CH;
-    uint32_t pieces = 0;
+    uint32_t pieces = 0, tiles = 0, ph = 0;
+    int slot = 0;
+    const bool withhold = prm.stall != 0 && blockIdx.x == 0;
     bool ok = true;
     while (ok) {
       const Piece* w = take();
       ok = w != nullptr;
       if (!ok || w->t1 == 0) break;
+      const int t0 = w->t0, t1 = w->t1, lo_tile = w->t.lo_tile, sink_tiles = w->t.sink_tiles;
+      const k8::Sight sight = w->t.sight;
+      const int piece_head = w->head, piece_b = w->b;
       const int r0 = w->t.r0, rows = w->t.rows, first = w->t.first, head0 = w->head * p.group;
       release();
       if (pieces > 0) ok = warp_wait(&ctrl->q_empty, (pieces - 1) & 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
@@ -645,6 +673,88 @@ __global__ void __launch_bounds__(THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->q_full);
+      if (C::INT4) {   // the piece's key and value tiles, unpacked into the ring
+        for (int i = t0; i < t1 && ok; ++i, ++tiles) {
+          const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
+          const int at = tiles % C::AFFINES;
+          ok = warp_wait(&ctrl->a_empty[at], ((tiles / C::AFFINES) & 1u) ^ 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
+          if (!ok) break;
+          // pages of the tile's eight runs of 16 keys, looked up by lanes 0-7
+          int page = -1;
+          if (lane < TILE / 16) {
+            const int k = key + lane * 16;
+            if (k < sight.len && (k + 16 > sight.lo || k < sight.sinks)) page = kv_page(p.kv, piece_b, k);
+          }
+#pragma unroll 1
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            // scales: two keys a thread
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c2 = 2 * t + e, k = key + c2;
+              const int id = __shfl_sync(0xffffffffu, page, c2 >> 4);
+              float sc = 0.f, off = 0.f;
+              if (id >= 0 && sight.any(k)) {
+                const uint32_t pair = __ldg((kv ? p.kv.v_scale : p.kv.k_scale) + id * p.kv.scale_stride + kv_row_in_page(p.kv, piece_head, k));
+                sc = kv_scale_of(pair);
+                off = fmaf(8.f, sc, kv_min_of(pair));
+                if (!kv) {   // the scores in base 2
+                  sc *= p.scale_log2;
+                  off *= p.scale_log2;
+                }
+              }
+              float* a = reinterpret_cast<float*>(affine + at * C::AFFINE_TILE + kv * (TILE * 8)) + t * 4;
+              a[e] = sc;
+              a[2 + e] = off;
+            }
+            ok = warp_wait(&ctrl->empty[slot], ph ^ 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
+            if (!ok) break;
+            // codes: 16 bytes (32 values) a load, D / 32 lanes a row
+            constexpr int LR = D / 32, PASS = 64 / LR;   // lanes of a row, rows of a pass
+            const int lr = t % LR, row0 = t / LR;
+            const uint32_t dst = smem_u32(ring) + slot * C::TILE_BYTES + (lr >> 1) * C::HALF_BYTES;
+            const uint8_t* base = kv ? p.kv.v : p.kv.k;
+#pragma unroll 1
+            for (int r = 0; r < TILE; r += 4 * PASS) {
+              uint4 x[4];
+              uint32_t got = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int row = r + e * PASS + row0, k = key + row;
+                const int id = __shfl_sync(0xffffffffu, page, row >> 4);
+                x[e] = make_uint4(0, 0, 0, 0);
+                if (id >= 0 && sight.any(k)) {
+                  got |= 1u << e;
+                  x[e] = ldg16(base + id * p.kv.page_stride + static_cast<long long>(kv_row_in_page(p.kv, piece_head, k)) * (D / 2) + lr * 16);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int row = r + e * PASS + row0;
+                const uint32_t words[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint32_t y = words[q];   // code - 8 of its eight codes, in order
+                  const uint32_t a = k8::code_pair8(y), b = k8::code_pair8(y >> 4), c = k8::code_pair8(y >> 8), d = k8::code_pair8(y >> 12);
+                  uint4 o = make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410), __byte_perm(a, b, 0x7632),
+                                       __byte_perm(c, d, 0x7632));
+                  if (!(got >> e & 1u)) o = make_uint4(0, 0, 0, 0);
+                  st_shared_v4(dst + row * 128 + (((((lr & 1) << 2) + q) ^ (row & 7)) << 4), o);
+                }
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (kv) mbar_arrive(&ctrl->a_full[at]);
+              if (!(withhold && tiles == 0 && kv == 0)) mbar_arrive(&ctrl->full[slot]);
+            }
+            if (++slot == C::STAGES) {
+              slot = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -655,7 +765,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t ts = tmem + lanes + C::S0 + s * TILE, to = tmem + lanes + C::O0 + s * D;
     const float scale = p.scale_log2;
     uint32_t done = 0, outs = 0;   // tiles and pieces of this sub-tile so far
-    uint32_t joins = 0;
+    uint32_t joins = 0, before = 0;   // before: tiles of the earlier pieces
     auto join = [&]() {            // a bounded barrier of the 8 softmax warps
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->join);
@@ -673,6 +783,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int w0 = w->t.pos_first + min(r0 + s * TILE + quarter * 32, rows - 1) / p.group;
       const int w1 = w->t.pos_first + min(r0 + s * TILE + quarter * 32 + 31, rows - 1) / p.group;
       const int lo_tile = w->t.lo_tile, sink_tiles = w->t.sink_tiles;
+      float qsum = 0.f;        // 4-bit pages: the row's sum of q
+      f32x2 corr2 = pk2(0.f, 0.f);   // and sum of p (minimum + 8 scale)
+      if (C::INT4) {
+        const bf16* src = p.q + (static_cast<long long>(w->head * p.group + rr % p.group) * p.kv.M + w->t.first + rr / p.group) * D;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 8) {
+          float f[8];
+          unpack8(ldg16(src + d), f);
+          qsum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+        }
+      }
+      const int t1 = w->t1;
       float top = -INFINITY;   // the maximum that the sum and the accumulators are relative to
       f32x2 sum2 = pk2(0.f, 0.f);
       for (int i = t0; i < end && ok; ++i, ++done) {
@@ -683,6 +805,24 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int c = 0; c < TILE; c += 32) tmem_ld32(ts + c, x + c);
         tmem_ld_wait();
+        const uint32_t at = (before + (i - t0)) % C::AFFINES;
+        const uint32_t ak = smem_u32(affine) + at * C::AFFINE_TILE;
+        if (C::INT4) {   // s (q . (c - 8)) + (m + 8 s) sum(q), in base 2 already
+          ok = warp_wait(&ctrl->a_full[at], ((before + (i - t0)) / C::AFFINES) & 1u, abortf, status, kStatusWaitConv, p.wait_ns);
+          if (!ok) break;
+          const f32x2 qs2 = pk2(qsum, qsum);
+#pragma unroll
+          for (int c = 0; c < TILE; c += 2) {
+            const uint4 a = ld_shared_v4(ak + c * 8);
+            const f32x2 y = fma2(pk2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+                                 pk2(__uint_as_float(a.x), __uint_as_float(a.y)),
+                                 mul2(pk2(__uint_as_float(a.z), __uint_as_float(a.w)), qs2));
+            float y0, y1;
+            unpk2(y, y0, y1);
+            x[c] = __float_as_uint(y0);
+            x[c + 1] = __float_as_uint(y1);
+          }
+        }
         const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
         // some row of the warp does not see some key
         if (key + TILE - 1 > w0 || (p.window > 0 && key <= w1 - p.window && key + TILE > p.sinks)) {
@@ -702,7 +842,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int c = 8; c < TILE; c += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + 4 + e]));
-        const float m = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * scale;
+        const float m = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * (C::INT4 ? 1.f : scale);
         if (__any_sync(0xffffffffu, m > top + GROWTH)) {
           const bool grow = m > top + GROWTH;
           const float f = grow && top != -INFINITY ? k8::ex2(top - m) : 1.f;
@@ -710,6 +850,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           float a, c;
           unpk2(sum2, a, c);
           sum2 = pk2(a * f, c * f);
+          if (C::INT4) corr2 = mul2(corr2, pk2(f, f));
           if (i > t0 && __any_sync(0xffffffffu, f != 1.f)) {   // (before the first product O holds nothing)
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 16) {
@@ -730,7 +871,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t w[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            f32x2 y = fma2(pk2(__uint_as_float(x[h * 32 + 2 * c]), __uint_as_float(x[h * 32 + 2 * c + 1])), scale2, base2);
+            const f32x2 z = pk2(__uint_as_float(x[h * 32 + 2 * c]), __uint_as_float(x[h * 32 + 2 * c + 1]));
+            f32x2 y = C::INT4 ? add2(z, base2) : fma2(z, scale2, base2);
             float a, d;
             unpk2(y, a, d);
             a = k8::ex2(a);
@@ -738,6 +880,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             y = pk2(a, d);
             if (c & 1) part2 = add2(part2, y);
             else sum2 = add2(sum2, y);
+            if (C::INT4) {   // p s goes to the product, p (m + 8 s) is added at the end
+              const uint4 v = ld_shared_v4(ak + TILE * 8 + (h * 32 + 2 * c) * 8);
+              corr2 = fma2(y, pk2(__uint_as_float(v.z), __uint_as_float(v.w)), corr2);
+              unpk2(mul2(y, pk2(__uint_as_float(v.x), __uint_as_float(v.y))), a, d);
+            }
             w[c] = pack_bf16x2(a, d);
           }
           tmem_st16(ts + h * 16, w);
@@ -747,11 +894,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->p_full[s]);
+        if (C::INT4 && lane == 0) mbar_arrive(&ctrl->a_empty[at]);
+      }
+      if (C::INT4) {   // tiles that this sub-tile does not reach
+        for (int i = max(end, t0); i < t1 && ok; ++i) {
+          const uint32_t at = (before + (i - t0)) % C::AFFINES;
+          ok = warp_wait(&ctrl->a_full[at], ((before + (i - t0)) / C::AFFINES) & 1u, abortf, status, kStatusWaitConv, p.wait_ns);
+          if (ok && lane == 0) mbar_arrive(&ctrl->a_empty[at]);
+        }
+        before += t1 - t0;
       }
       // ---- the piece's result
       float a, c;
       unpk2(sum2, a, c);
       float sum = a + c;
+      unpk2(corr2, a, c);
+      const float corr = a + c;
       if (ok && t0 < end) {
         ok = warp_wait(&ctrl->o_full[s], outs & 1u, abortf, status, kStatusWaitTmemFull, p.wait_ns);
         ++outs;
@@ -787,7 +945,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           // (a row without keys, and a sub-tile without tiles, have no accumulators)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) f[e] = sum > 0.f ? __uint_as_float(o[e]) : 0.f;
+          for (int e = 0; e < 16; ++e) f[e] = sum > 0.f ? __uint_as_float(o[e]) + (C::INT4 ? corr : 0.f) : 0.f;
           if (r < rows) {
             if (whole) {
               put(d0, f, sum > 0.f ? 1.f / sum : 0.f);
