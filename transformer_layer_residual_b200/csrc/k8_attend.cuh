@@ -788,23 +788,42 @@ __global__ void __launch_bounds__(SplitCfg<D, FMT, NR>::THREADS, SplitCfg<D, FMT
       __syncthreads();
       if (found[2]) {
         __threadfence();
+        // four parts' loads at a time (a head over every block has dozens of parts)
+        constexpr int AT_ONCE = 4;
+        auto slot_of = [&](int c) { return p.part + static_cast<long long>(2 * c + (c == c0)) * kPartFloats; };
         top = -INFINITY;
-        for (int c = c0; c <= c1; ++c)
-          top = fmaxf(top, __ldcg(p.part + static_cast<long long>(2 * c + (c == c0)) * kPartFloats + C::ROWS * D + row));
+        for (int c = c0; c <= c1; c += AT_ONCE) {
+          float x[AT_ONCE];
+#pragma unroll
+          for (int k = 0; k < AT_ONCE; ++k) x[k] = __ldcg(slot_of(min(c + k, c1)) + C::ROWS * D + row);
+#pragma unroll
+          for (int k = 0; k < AT_ONCE; ++k) top = fmaxf(top, x[k]);
+        }
         sum = 0.f;
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-          const float* s = p.part + static_cast<long long>(2 * c + (c == c0)) * kPartFloats;
-          const float f = top == -INFINITY ? 0.f : ex2(__ldcg(s + C::ROWS * D + row) - top);
-          sum += f * __ldcg(s + C::ROWS * D + C::ROWS + row);
+        for (int c = c0; c <= c1; c += AT_ONCE) {
+          float f[AT_ONCE], l[AT_ONCE];
+          float4 x[AT_ONCE][PER / 4];
 #pragma unroll
-          for (int e = 0; e < PER; e += 4) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(s + row * D + d0 + e));
-            acc[e] = fmaf(f, x.x, acc[e]);
-            acc[e + 1] = fmaf(f, x.y, acc[e + 1]);
-            acc[e + 2] = fmaf(f, x.z, acc[e + 2]);
-            acc[e + 3] = fmaf(f, x.w, acc[e + 3]);
+          for (int k = 0; k < AT_ONCE; ++k) {
+            const float* s = slot_of(min(c + k, c1));
+            f[k] = __ldcg(s + C::ROWS * D + row);
+            l[k] = __ldcg(s + C::ROWS * D + C::ROWS + row);
+#pragma unroll
+            for (int e = 0; e < PER / 4; ++e) x[k][e] = __ldcg(reinterpret_cast<const float4*>(s + row * D + d0) + e);
+          }
+#pragma unroll
+          for (int k = 0; k < AT_ONCE; ++k) {
+            const float g = top == -INFINITY || c + k > c1 ? 0.f : ex2(f[k] - top);
+            sum = fmaf(g, l[k], sum);
+#pragma unroll
+            for (int e = 0; e < PER / 4; ++e) {
+              acc[4 * e] = fmaf(g, x[k][e].x, acc[4 * e]);
+              acc[4 * e + 1] = fmaf(g, x[k][e].y, acc[4 * e + 1]);
+              acc[4 * e + 2] = fmaf(g, x[k][e].z, acc[4 * e + 2]);
+              acc[4 * e + 3] = fmaf(g, x[k][e].w, acc[4 * e + 3]);
+            }
           }
         }
         if (works && row < sight.rows) store_row_part<D, PER>(p, st.first, head, row, d0, acc, top, sum);

@@ -975,8 +975,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (ok && ctrl->last) {
           __threadfence();
           if (r < rows) {
+            // four parts' loads at a time
+            constexpr int AT_ONCE = 4;
             top = -INFINITY;
-            for (int k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(slot_of(k) + ROWS * D + row));
+            for (int k = c0; k <= c1; k += AT_ONCE) {
+              float x[AT_ONCE];
+#pragma unroll
+              for (int e = 0; e < AT_ONCE; ++e) x[e] = __ldcg(slot_of(min(k + e, c1)) + ROWS * D + row);
+#pragma unroll
+              for (int e = 0; e < AT_ONCE; ++e) top = fmaxf(top, x[e]);
+            }
             sum = 0.f;
             for (int k = c0; k <= c1; ++k)
               sum += (top == -INFINITY ? 0.f : k8::ex2(__ldcg(slot_of(k) + ROWS * D + row) - top)) *
@@ -986,15 +994,26 @@ __global__ void __launch_bounds__(THREADS, 1)
               float acc[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-              for (int k = c0; k <= c1; ++k) {
-                const float f = top == -INFINITY ? 0.f : k8::ex2(__ldcg(slot_of(k) + ROWS * D + row) - top);
+              for (int k = c0; k <= c1; k += AT_ONCE) {
+                float4 y[AT_ONCE][4];
+                float f[AT_ONCE];
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                  const float4 y = __ldcg(reinterpret_cast<const float4*>(slot_of(k)) + ((d0 + e) >> 2) * ROWS + row);
-                  acc[e] = fmaf(f, y.x, acc[e]);
-                  acc[e + 1] = fmaf(f, y.y, acc[e + 1]);
-                  acc[e + 2] = fmaf(f, y.z, acc[e + 2]);
-                  acc[e + 3] = fmaf(f, y.w, acc[e + 3]);
+                for (int q = 0; q < AT_ONCE; ++q) {
+                  const float* from = slot_of(min(k + q, c1));
+                  f[q] = __ldcg(from + ROWS * D + row);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) y[q][e] = __ldcg(reinterpret_cast<const float4*>(from) + (d0 / 4 + e) * ROWS + row);
+                }
+#pragma unroll
+                for (int q = 0; q < AT_ONCE; ++q) {
+                  const float g = top == -INFINITY || k + q > c1 ? 0.f : k8::ex2(f[q] - top);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    acc[4 * e] = fmaf(g, y[q][e].x, acc[4 * e]);
+                    acc[4 * e + 1] = fmaf(g, y[q][e].y, acc[4 * e + 1]);
+                    acc[4 * e + 2] = fmaf(g, y[q][e].z, acc[4 * e + 2]);
+                    acc[4 * e + 3] = fmaf(g, y[q][e].w, acc[4 * e + 3]);
+                  }
                 }
               }
               put(d0, acc, sum > 0.f ? 1.f / sum : 0.f);
