@@ -64,16 +64,30 @@ __device__ __forceinline__ void row_min_max(const float (&a)[8], const float (&b
   }
 }
 
-__device__ __forceinline__ uint32_t codes8(const float (&x)[8], float lo, float s) {
-  uint32_t w = 0;
-  if (s > 0.f) {
+// Codes round((x - lo) / s) of eight values, the first in the low nibble. The
+// quotient's nearest integer comes from the product with 1 / s and is right wherever
+// the remainder stays clear of half a step, which the remainder, exact in one fma,
+// shows; else (ties and their neighbours) the quotient itself is rounded. Integers
+// are taken from floats by adding 1.5 * 2^23, four codes at a time.
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8], float lo, float s, float inv) {
+  constexpr float kMagic = 12582912.f;
+  if (!(s > 0.f)) return 0u;
+  const float clear = s * 0.4999995f;
+  float c[8];
+  bool near = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], lo), s)), 0.f), 15.f);
-      w |= static_cast<uint32_t>(c) << (4 * i);
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float t = __fsub_rn(x[i], lo);
+    c[i] = __fsub_rn(fmaf(t, inv, kMagic), kMagic);
+    near |= !(fabsf(fmaf(-c[i], s, t)) < clear);   // (also where a value or 1 / s is not finite)
   }
-  return w;
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], lo), s)), 0.f), 15.f);
+  }
+  const float w0 = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]) + kMagic;
+  const float w1 = fmaf(fmaf(fmaf(c[7], 16.f, c[6]), 16.f, c[5]), 16.f, c[4]) + kMagic;
+  return __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x5410);
 }
 
 template <int D, int FMT, bool INTERLEAVED>
@@ -161,19 +175,20 @@ __global__ void __launch_bounds__(kKvThreads) k7_append(const __grid_constant__ 
         x0[i] = pack8(ya);
         x1[i] = pack8(yd);
       }
-      if (FMT == kKvInt4) {
+      if (FMT == kKvInt4 && __any_sync(0xffffffffu, r >= p.Hq && r < rows)) {   // (q rows are not coded)
         float a[8], d[8], lo, hi;
         unpack8(x0[i], a);
         unpack8(x1[i], d);
         row_min_max<LANES>(a, d, lo, hi);
         // (max - min) / 15, rounded up to bf16: any bit below the upper half carries into it
         const float s = __uint_as_float((__float_as_uint(__fdiv_rn(__fsub_rn(hi, lo), 15.f)) + 0xFFFFu) & 0xFFFF0000u);
+        const float inv = __fdiv_rn(1.f, s);
         if (live && page >= 0 && r >= p.Hq && r < rows) {
           const int h = is_v ? r - p.Hq - Hkv : r - p.Hq;
           const int row = (h << p.kv.page_shift) + row_in_page;
           uint8_t* dst = (is_v ? p.kv.v : p.kv.k) + page * p.kv.page_stride + static_cast<long long>(row) * (D / 2);
-          *reinterpret_cast<uint32_t*>(dst + (e0 >> 1)) = codes8(a, lo, s);
-          *reinterpret_cast<uint32_t*>(dst + (e1 >> 1)) = codes8(d, lo, s);
+          *reinterpret_cast<uint32_t*>(dst + (e0 >> 1)) = codes8(a, lo, s, inv);
+          *reinterpret_cast<uint32_t*>(dst + (e1 >> 1)) = codes8(d, lo, s, inv);
           if (c == 0)
             (is_v ? p.kv.v_scale : p.kv.k_scale)[page * p.kv.scale_stride + row] =
                 (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
