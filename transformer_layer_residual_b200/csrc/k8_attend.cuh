@@ -457,17 +457,24 @@ template <int D, int FMT, int NR>
 struct SplitCfg {
   static constexpr bool BULK = FMT == kKvInt4;                 // bulk copies (else 16-byte asynchronous ones)
   static constexpr int ROWS = NR * 8;                          // rows of a piece
-  static constexpr int KEYS = 32;                              // keys of a warp's step
-  static constexpr int WARPS = FMT == kKvBf16 ? 4 : (NR == 1 ? 8 : 12);
-  static constexpr int STAGES = 3;
+  // keys of a warp's step, warps, steps in the ring, resident blocks of an SM: chosen
+  // by measurement. bf16 pages are bound by memory: 192 KB of ring, two thirds of it
+  // in flight. 4-bit pages are bound by unpacking: 64-key steps (fewer loop and copy
+  // instructions) with as many warps as their registers leave, two blocks of 6 for 8
+  // rows (64 sequences of 2000 to 12000: 138 us; 32-key steps with 16 warps 150, with
+  // 8 warps 181), one of 8 for 16 rows, whose state is twice as large (130003 keys:
+  // 68 us; two blocks of 6 98, 32-key steps with 12 warps 83).
+  static constexpr int KEYS = FMT == kKvBf16 ? 32 : 64;
+  static constexpr int WARPS = FMT == kKvBf16 ? 4 : (NR == 1 ? 6 : 8);
+  static constexpr int STAGES = FMT == kKvBf16 ? 3 : 2;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int TILE = KEYS * WARPS;                    // keys of a unit
   typedef Tile<D, FMT, KEYS> Layout;
   static constexpr int RING = WARPS * STAGES * Layout::kBytes;
   static constexpr int MERGE = WARPS * ROWS * (D + 2) * 4;     // the merge buffer reuses the ring
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE);
-  // resident blocks of an SM
-  static constexpr int BLOCKS = 2 * (SMEM + 1536) <= 227 * 1024 && (FMT == kKvBf16 || NR == 1) ? 2 : 1;
+  static constexpr int BLOCKS = FMT == kKvBf16 ? (D == 128 ? 1 : 2) : (NR == 1 ? 2 : 1);
+  static_assert(BLOCKS * (SMEM + 1536) <= 227 * 1024, "shared memory of an SM");
 };
 
 // Bulk copies of warp steps of 4-bit pages. A step is up to KEYS / 16 runs of
@@ -672,7 +679,7 @@ __global__ void __launch_bounds__(SplitCfg<D, FMT, NR>::THREADS, SplitCfg<D, FMT
       ++issued;
       page = i + 1 < t1 ? bulk.page(p.kv, b, key_of(i + 1), sight) : -1;
     };
-    if (C::BULK) {
+    if constexpr (C::BULK) {
       page = bulk.page(p.kv, b, key_of(t0), sight);
       for (int i = t0; i < min(t0 + C::STAGES, t1); ++i) issue(i);
     } else {
@@ -700,7 +707,7 @@ __global__ void __launch_bounds__(SplitCfg<D, FMT, NR>::THREADS, SplitCfg<D, FMT
       const int key = key_of(i);
       // a step none of whose keys is seen is skipped (behind the end, between sinks and window)
       const bool any = key < st.len && (key + C::KEYS > st.lo || key < p.sinks);
-      if (C::BULK) {
+      if constexpr (C::BULK) {
         const uint32_t at = used % C::STAGES;
         ok = warp_wait(&full[warp][at], (used / C::STAGES) & 1, &abort_flag, p.kv.status, kStatusWaitFull, p.wait_ns);
         if (!ok) break;
