@@ -316,10 +316,13 @@ fnl_status fnl_linear_add_residual(fnl_handle* h, fnl_stream stream, const fnl_b
  *                scale s and minimum lo. A code c in 0..15 stands for lo + c s.
  * A row is coded by lo = min x, s = (max x - lo) / 15 rounded up to bf16,
  * c = round((x - lo) / s) (to nearest even, in fp32; 0 where s = 0): every value
- * is within s / 2 of what its code stands for. Rows have to be finite.
+ * is within s / 2 of what its code stands for. Rows have to be finite, and so has
+ * max x - min x in fp32.
  * Pages may lie apart: page_stride bytes from page to page in k and in v (0:
  * dense), scale_page_stride in the scales (0: dense), both multiples of 16, so that
- * k and v may be the halves of one [num_pages, 2, ...] allocation. */
+ * k and v may be the halves of one [num_pages, 2, ...] allocation. The calls on one
+ * handle share its work counters and partial sums, also as graphs captured from it:
+ * they run one at a time (a second stream takes a second handle). */
 typedef enum { FNL_KV_BF16 = 0, FNL_KV_INT4 = 1 } fnl_kv_format;
 
 typedef struct {
@@ -372,7 +375,8 @@ typedef struct {
  * rot_dim = 0: no rotation; q, q_out, cos and sin must then be NULL. One kernel.
  * Errors: FNL_ERR_INVALID_ARG, FNL_ERR_ALIGNMENT (16 bytes for tensors, 4 for
  * integer lists), FNL_ERR_ALIAS (q_out partly on q, or a tensor on the
- * cache), FNL_ERR_UNSUPPORTED (D, page_size, B > 65535). */
+ * cache, or k, v and their scales on one another), FNL_ERR_UNSUPPORTED (D, page_size,
+ * B > 65535). */
 fnl_status fnl_rope_append_kv(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch,
                               int M, int Hq, const fnl_bf16* q, const fnl_bf16* k, const fnl_bf16* v,
                               const float* cos, const float* sin, int rot_dim, int max_pos, int interleaved,
@@ -398,7 +402,9 @@ fnl_status fnl_kv_gather(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* c
  * read, whatever they hold; visible ones have to be finite.
  * Any mix of lengths is correct; a batch of few new tokens per sequence (at most
  * 16 rows max_q * Hq / Hkv) runs the form that splits the keys over the whole GPU,
- * so decode steps and prompts are best given as two calls. */
+ * so decode steps and prompts are best given as two calls. Limits
+ * (FNL_ERR_UNSUPPORTED): max_pages * page_size <= 2^30 positions; B <= 16384 above
+ * 16 rows max_q * Hq / Hkv. */
 fnl_status fnl_paged_attention(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch,
                                int M, int Hq, const fnl_bf16* q, float scale, int window, int sinks, fnl_bf16* out,
                                float* lse);

@@ -515,3 +515,101 @@ def test_prompts_of_many_sequences(handle):
     c = Cache("bf16", [6000, 50, 2900], 2, 128, 128, seed=62)
     _check_attention(handle, c, [20, 30, 0], 8)
     _check_attention(handle, c, [40, 1, 70], 8, window=1500, sinks=200)
+
+
+def test_refusals_of_overlapping_pages(handle):
+    """Pages that lie on one another: refused where they would be written, allowed where
+    they are read (keys that are the values as well)."""
+    Hkv, page, D = 2, 16, 64
+    n = Hkv * page * D
+    buf = torch.zeros(9 * n, dtype=torch.bfloat16, device="cuda")
+    tab = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    batch = fnl.KVBatch(_cu([2]), _i32([2]), tab, 2)
+    q = torch.zeros(4, 2, D, dtype=torch.bfloat16, device="cuda")
+    k = torch.ones(2, 2, D, dtype=torch.bfloat16, device="cuda")
+
+    def pages(first, stride, count=4):
+        return buf[first:].as_strided((count, Hkv, page, D), (stride, page * D, D, 1))
+
+    with pytest.raises(ValueError, match="overlap"):
+        fnl.KVCache(buf[:n].view(1, Hkv, page, D).expand(4, -1, -1, -1), pages(0, n))
+    with pytest.raises(ValueError, match="overlap"):
+        fnl.KVCache(pages(0, n - 16), pages(0, n - 16))
+    for a, b in ((pages(0, n), pages(0, n)), (pages(0, n), pages(3 * n + n // 2, n)), (pages(3 * n + 16, n), pages(0, n)),
+                 (pages(0, 2 * n), pages(n - 8, 2 * n)), (pages(n + 8, 2 * n), pages(0, 2 * n))):
+        with pytest.raises(fnl.FnlError) as e:
+            fnl.rope_append_kv(handle, fnl.KVCache(a, b), batch, None, k, k)
+        assert e.value.status == 3, e.value
+    for a, b in ((pages(0, n), pages(4 * n, n)), (pages(0, 2 * n), pages(n, 2 * n)), (pages(n, 2 * n), pages(0, 2 * n))):
+        fnl.rope_append_kv(handle, fnl.KVCache(a, b), batch, None, k, k)
+    same = fnl.KVCache(pages(0, n), pages(0, n))
+    pages(0, n)[:] = 3.0
+    assert torch.all(fnl.paged_attention(handle, same, batch, q)["out"] == 3.0)
+    c = fnl.KVCache.empty(4, page, Hkv, D, "int4")
+    with pytest.raises(fnl.FnlError) as e:
+        fnl.rope_append_kv(handle, fnl.KVCache(c.k, c.v, c.k_scale, c.k_scale), batch, None, k, k)
+    assert e.value.status == 3, e.value
+    # more positions than the key tiles' counts hold
+    far = fnl.KVBatch(_cu([2]), _i32([2]), torch.zeros(1, (1 << 26) + 1, dtype=torch.int32, device="cuda"), 2)
+    with pytest.raises(fnl.FnlError) as e:
+        fnl.paged_attention(handle, same, far, q)
+    assert e.value.status == 4, e.value
+    handle.check()
+
+
+@FMT
+def test_prompts_in_a_replayed_graph(cuda_device, fmt):
+    """The tensor-core form captured as a handle's first call, replayed on other lengths
+    (an empty sequence, no sequence longer than a row tile, one of every block's) and
+    between eager calls of the split form on the same handle and stream."""
+    Hq, Hkv, D, page, B, M = 8, 2, 64, 16, 3, 700
+    c = Cache(fmt, [900, 700, 400], Hkv, D, page, seed=70)
+    cache, tab = _dev(c)
+    h, h0 = fnl.Handle(0), fnl.Handle(0)
+    q = torch.randn(Hq, M, D, generator=torch.Generator().manual_seed(71)).to(torch.bfloat16).cuda()
+    cu, kv = _cu([300, 200, 200]), _i32(c.lens)
+    batch = fnl.KVBatch(cu, kv, tab, 500)
+    out = torch.empty(M, Hq * D, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        fnl.paged_attention(h, cache, batch, q, out=out, window=300, sinks=3)
+    one = fnl.KVBatch(_cu([1, 1, 1]), _i32(c.lens), tab, 1)
+    for new, lens in (([300, 200, 200], [900, 700, 400]), ([500, 0, 7], [600, 700, 7]), ([1, 1, 1], [1, 650, 399]),
+                      ([0, 0, 0], [5, 5, 5])):
+        want = torch.full_like(out, 7.0)
+        fnl.paged_attention(h0, cache, fnl.KVBatch(_cu(new), _i32(lens), tab, 500), q, out=want, window=300, sinks=3)
+        first = fnl.paged_attention(h0, cache, one, q[:, :3].contiguous())["out"]
+        cu.copy_(_cu(new))
+        kv.copy_(_i32(lens))
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+            got = fnl.paged_attention(h, cache, one, q[:, :3].contiguous())["out"]
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(got, first), new
+    h.check()
+    h0.check()
+    h.close()
+    h0.close()
+
+
+@FMT
+@pytest.mark.parametrize("n", [1, 40])
+def test_sequences_that_share_pages(handle, fmt, n):
+    """A common prefix kept once: the same bits as from copies of its pages."""
+    Hq, Hkv, D, page = 8, 2, 64, 32
+    c = Cache(fmt, [256 + n, 256 + n], Hkv, D, page, seed=80)
+    cache, tab = _dev(c)
+    q = torch.randn(Hq, 2 * n, D, generator=torch.Generator().manual_seed(81)).to(torch.bfloat16).cuda()
+    shared = tab.clone()
+    shared[1, :8] = tab[0, :8]
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        if t is not None:
+            t[tab[1, :8].long()] = t[tab[0, :8].long()]
+    outs = [fnl.paged_attention(handle, cache, fnl.KVBatch(_cu([n, n]), _i32(c.lens), x, n), q)["out"] for x in (tab, shared)]
+    handle.check()
+    assert torch.equal(*outs)

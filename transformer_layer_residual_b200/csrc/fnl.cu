@@ -1141,6 +1141,8 @@ fnl_status fnl_create(fnl_handle** out, int device, const fnl_options* opt) {
     return FNL_ERR_INVALID_ARG;
   }
   h->device = device;
+  h->page_maps.e.reserve(PageMaps::kSize);   // (so that the paged-cache calls do not allocate)
+  h->plan_text.reserve(256);
   cudaError_t e = cudaSetDevice(device);
   if (e != cudaSuccess) {
     delete h;
@@ -1490,6 +1492,35 @@ fnl_status cache_alias(fnl_handle* h, const fnl_kv_cache* c, const fnl_kv_batch*
   return FNL_OK;
 }
 
+// Whether a page at a + i * sa (bytes na) and one at b + j * sb (bytes nb) overlap for some i, j < n. Pages of
+// different strides that cannot be told apart by their spans count as overlapping.
+bool pages_overlap(const void* a, long long na, long long sa, const void* b, long long nb, long long sb, int n) {
+  const long long d = static_cast<long long>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  if (d >= (n - 1) * sa + na || -d >= (n - 1) * sb + nb) return false;
+  if (sa != sb) return true;
+  const long long r = (d % sa + sa) % sa;   // b's page lies r behind one of a's, sa - r before the next
+  return r < na || sa - r < nb;
+}
+// An append writes k, v and their scales: none of them may lie on another.
+fnl_status cache_parts_apart(fnl_handle* h, const fnl_kv_cache* c, const KvParams& p) {
+  const long long rows = static_cast<long long>(c->Hkv) * c->page_size;
+  const bool int4 = c->format == FNL_KV_INT4;
+  const long long bytes = rows * (int4 ? c->D / 2 : 2 * c->D);
+  const struct {
+    const void* ptr;
+    long long bytes, stride;
+    const char* name;
+  } part[] = {{c->k, bytes, p.page_stride, "k"},
+              {c->v, bytes, p.page_stride, "v"},
+              {c->k_scale, rows * 4, p.scale_stride * 4, "k_scale"},
+              {c->v_scale, rows * 4, p.scale_stride * 4, "v_scale"}};
+  for (int i = 0; i < (int4 ? 4 : 2); ++i)
+    for (int j = 0; j < i; ++j)
+      if (pages_overlap(part[j].ptr, part[j].bytes, part[j].stride, part[i].ptr, part[i].bytes, part[i].stride, c->num_pages))
+        return fail(h, FNL_ERR_ALIAS, "the cache's %s overlaps its %s", part[i].name, part[j].name);
+  return FNL_OK;
+}
+
 template <typename Kern, typename Params>
 fnl_status kv_launch(fnl_handle* h, Kern kern, dim3 grid, int threads, int smem, cudaStream_t stream, const Params& p) {
   fnl_status st = FNL_OK;
@@ -1644,6 +1675,7 @@ fnl_status fnl_rope_append_kv(fnl_handle* h, fnl_stream stream, const fnl_kv_cac
   const size_t tq = static_cast<size_t>(Hq) * M * cache->D * 2, tk = static_cast<size_t>(cache->Hkv) * M * cache->D * 2;
   const size_t tab = static_cast<size_t>(std::max(max_pos, 0)) * rot_dim * 2;
   const Range io[] = {{q_out, tq, "q_out"}, {q, tq, "q"}, {k, tk, "k"}, {v, tk, "v"}, {cos, tab, "cos"}, {sin, tab, "sin"}};
+  if (cache->num_pages > 0 && (st = cache_parts_apart(h, cache, p.kv)) != FNL_OK) return st;
   if ((st = cache_alias(h, cache, batch, p.kv, io, 6)) != FNL_OK) return st;
   for (int i = 1; i < 6; ++i)
     if (!(i == 1 && q_out == q) && overlap(io[0], io[i]))
@@ -1695,6 +1727,9 @@ fnl_status fnl_paged_attention(fnl_handle* h, fnl_stream stream, const fnl_kv_ca
     return fail(h, FNL_ERR_INVALID_ARG, "window and sinks must be >= 0, and sinks need a window");
   if (static_cast<long long>(batch->max_q) * (Hq / cache->Hkv) > 0x7fffff00LL)
     return fail(h, FNL_ERR_UNSUPPORTED, "max_q * Hq / Hkv must stay below 2^31 - 256 rows");
+  const long long positions = static_cast<long long>(batch->max_pages) * cache->page_size;
+  if (positions > (1LL << 30) || batch->B * (positions / 128 + 2) > 0x7fffffffLL)   // key tiles are counted in 32 bits
+    return fail(h, FNL_ERR_UNSUPPORTED, "need max_pages * page_size <= 2^30 and B of them below 2^38 positions");
   if (M == 0 || batch->B == 0) return FNL_OK;
   if (batch->max_q == 0) return fail(h, FNL_ERR_INVALID_ARG, "max_q must be > 0 for a batch with tokens");
   if (!q || !out) return fail(h, FNL_ERR_INVALID_ARG, "q and out are required");

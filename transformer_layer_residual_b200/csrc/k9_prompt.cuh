@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (w == nullptr || w->t1 == 0) break;
       const int rows = w->t.rows, r0 = w->t.r0, r = r0 + row;
       const int t0 = w->t0, end = min(w->t1, s ? w->t.n1 : w->t.n0);
-      const int rr = min(r, rows - 1);
+      const int rr = max(min(r, rows - 1), 0);   // (rows is 0 only where the arrays change under the kernel)
       const int pos = w->t.pos_first + rr / p.group;
       // the warp's own span of positions, for its masks
       const int w0 = w->t.pos_first + min(r0 + s * TILE + quarter * 32, rows - 1) / p.group;

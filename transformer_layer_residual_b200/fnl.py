@@ -461,6 +461,8 @@ class KVCache:
         inner = (shape[2] * shape[3], shape[3], 1)
         if any(st != want for st, want, n in zip(t.stride()[1:], inner, shape[1:]) if n > 1):
             raise ValueError(f"{name} must be contiguous within a page")
+        if shape[0] > 1 and t.stride(0) < shape[1] * shape[2] * shape[3]:
+            raise ValueError(f"the pages of {name} overlap (page stride {t.stride(0)})")
         return t.stride(0) * t.element_size() if shape[0] > 1 else 0
 
     @classmethod
