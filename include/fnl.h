@@ -403,7 +403,7 @@ fnl_status fnl_kv_gather(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* c
  * Any mix of lengths is correct; a batch of few new tokens per sequence (at most
  * 16 rows max_q * Hq / Hkv) runs the form that splits the keys over the whole GPU,
  * so decode steps and prompts are best given as two calls. Limits
- * (FNL_ERR_UNSUPPORTED): max_pages * page_size <= 2^30 positions; B <= 16384 above
+ * (FNL_ERR_UNSUPPORTED): max_pages * page_size <= 2^29 positions; B <= 16384 above
  * 16 rows max_q * Hq / Hkv. */
 fnl_status fnl_paged_attention(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch,
                                int M, int Hq, const fnl_bf16* q, float scale, int window, int sinks, fnl_bf16* out,

@@ -1728,8 +1728,8 @@ fnl_status fnl_paged_attention(fnl_handle* h, fnl_stream stream, const fnl_kv_ca
   if (static_cast<long long>(batch->max_q) * (Hq / cache->Hkv) > 0x7fffff00LL)
     return fail(h, FNL_ERR_UNSUPPORTED, "max_q * Hq / Hkv must stay below 2^31 - 256 rows");
   const long long positions = static_cast<long long>(batch->max_pages) * cache->page_size;
-  if (positions > (1LL << 30) || batch->B * (positions / 128 + 2) > 0x7fffffffLL)   // key tiles are counted in 32 bits
-    return fail(h, FNL_ERR_UNSUPPORTED, "need max_pages * page_size <= 2^30 and B of them below 2^38 positions");
+  if (positions > (1LL << 29) || batch->B * (positions / 128 + 2) > 0x7fffffffLL)   // key tiles are counted in 32 bits
+    return fail(h, FNL_ERR_UNSUPPORTED, "need max_pages * page_size <= 2^29 and B of them below 2^38 positions");
   if (M == 0 || batch->B == 0) return FNL_OK;
   if (batch->max_q == 0) return fail(h, FNL_ERR_INVALID_ARG, "max_q must be > 0 for a batch with tokens");
   if (!q || !out) return fail(h, FNL_ERR_INVALID_ARG, "q and out are required");

@@ -16,7 +16,7 @@
 // few heads, close together: the copies' way through L2 is what a scattered order
 // loses on (ragged prompts ran 1.8 times longer with the heads side by side). Where
 // the tiles are long, whole ones only fill whole waves, and the (row tile, key tile)
-// units of the rest, or of all when there are fewer tiles than SMs, are dealt evenly
+// units of the rest (of all when there are fewer tiles than SMs) are dealt evenly
 // over the blocks. A block's
 // first and last pieces of those may be parts: they leave fp32 partial sums, and the
 // last block to arrive adds them in block order. Which block takes a whole tile does
@@ -42,11 +42,13 @@
 // the FMA pipe (1345 -> 1369 .. 1564 us with one pair in eight .. two), and the first
 // half of a tile's probabilities handed over early (1345 -> 1401 us).
 //
-// 4-bit pages: the copying warp only deals out the pieces; warps 2 and 3 unpack key and
-// value tiles as code - 8, which bf16 holds exactly, and put the rows' scales beside
-// them. The softmax applies them in fp32: s (q . (c - 8)) + (m + 8 s) sum(q) to the
-// scores, p s as the second product's operand and sum(p (m + 8 s)) added at the end,
-// as K8 does; neither keys nor values are rounded.
+// 4-bit pages: rows and scales arrive as they are by bulk copies; warps 2 and 3 unpack key and
+// value tiles as 128 + code and code - 8, which bf16 holds exactly, and put the rows'
+// scales beside them. The softmax applies them in fp32: s (q . (128 + c)) +
+// (m - 128 s) sum(q) to the scores, p s as the second product's operand and
+// sum(p (m + 8 s)) added at the end, as K8 does; neither keys nor values are rounded.
+// The codes of a word keep the order in which shifts and masks bring them out; Q's
+// rows are stored in that order of d and the result's are put back.
 //
 // Slots that no row of the piece sees are not copied (whole pages) or are zeroed
 // in V's tile before the product (rows), since 0 * NaN would reach the result;
@@ -163,11 +165,14 @@ struct Cfg {
   static constexpr int TILE_BYTES = TILE * D * 2;   // Q sub-tile, K tile, V tile: HALVES blocks of 128 x 64
   static constexpr int HALF_BYTES = TILE * 128;
   static constexpr int STAGES = (INT4 ? 4 : 5) * (D == 128 ? 1 : 2);
-  // 4-bit pages: scales of a tile's keys, then of its values, four tiles deep: for keys
+  // 4-bit pages: scales of a tile's keys, then of its values, three tiles deep: for keys
   // c, c + 1 the four floats (scale, scale, offset, offset)
-  static constexpr int AFFINE_TILE = 2 * TILE * 8, AFFINES = 4;
+  static constexpr int AFFINE_TILE = 2 * TILE * 8, AFFINES = 3;
   static constexpr int AFFINE = INT4 ? AFFINES * AFFINE_TILE : 0;
-  static constexpr int SMEM = 2 * TILE_BYTES + STAGES * TILE_BYTES + AFFINE + 1024 + CTRL_BYTES;
+  // and key or value tiles as they are in the pages, three deep: codes, then scale pairs
+  static constexpr int RAW_CODES = TILE * D / 2, RAW_TILE = RAW_CODES + TILE * 4, RAWS = INT4 ? 3 : 0;
+  static constexpr int SMEM = 2 * TILE_BYTES + STAGES * TILE_BYTES + AFFINE + RAWS * RAW_TILE + 1024 + CTRL_BYTES;
+  static_assert(SMEM <= 227 * 1024, "shared memory of a block");
   static constexpr uint32_t S0 = 0, O0 = 256;       // TMEM columns: S at 0 and 128 (P over it), O at 256 and 256 + D
   static_assert(2 * (kMaxSeqs + 1) * 4 <= STAGES * TILE_BYTES + AFFINE, "prefix sums in the ring");
 };
@@ -229,7 +234,7 @@ struct Piece {
 
 struct Ctrl {
   uint64_t full[10], empty[10], s_full[2], p_full[2], o_full[2], q_full, q_empty, work_full[2], work_empty[2], join, drain;
-  uint64_t a_full[4], a_empty[4];
+  uint64_t a_full[4], a_empty[4], raw_full[3], raw_empty[3];
   uint32_t tmem_base;
   uint32_t armed, armed_parity;   // ring slots with a copy issued, and the parity of each one's last
   int abort_flag;
@@ -266,7 +271,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + 2 * C::TILE_BYTES;
   uint8_t* affine = ring + C::STAGES * C::TILE_BYTES;
-  Ctrl* ctrl = reinterpret_cast<Ctrl*>(affine + C::AFFINE);
+  uint8_t* raw = affine + C::AFFINE;
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(raw + C::RAWS * C::RAW_TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abortf = &ctrl->abort_flag;
   int* status = p.kv.status;
@@ -284,6 +290,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int s = 0; s < C::AFFINES; ++s) {
       mbar_init(&ctrl->a_full[s], 2);
       mbar_init(&ctrl->a_empty[s], 8);
+    }
+    for (int s = 0; s < C::RAWS; ++s) {
+      mbar_init(&ctrl->raw_full[s], 1);
+      mbar_init(&ctrl->raw_empty[s], 2);
     }
     mbar_init(&ctrl->q_full, 2);
     mbar_init(&ctrl->q_empty, 1);
@@ -349,13 +359,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   const int early = R - late;
   const long long N = static_cast<long long>(R) * p.kv.Hkv, N1 = static_cast<long long>(early) * p.kv.Hkv;
-  // Whole waves of tiles are taken whole. The rest are shared in parts of six key tiles
-  // at least (a part costs its sums' way through memory, about 15 us, six key tiles'
-  // time), where there are fewer tiles than blocks or where that ends sooner than
-  // another wave, the longest of the rest.
-  const long long full = N / G * G;
+  // Of many tiles, whole waves are taken whole and the rest may be shared; of few (one a
+  // thread here) all may. They are, in parts of six key tiles at least (a part costs its
+  // sums' way through memory, about 8 us, some six key tiles' time), where that ends
+  // sooner than whole ones would: with the longest when every block has one at most,
+  // else about half of the longest after the even share. Against always sharing what
+  // fills no wave, four chunks of 25 tokens and one prompt of 900 over 4-bit pages
+  // (D = 128) took 30 and 49 us instead of 41 and 65; five prompts of 172 row tiles, up
+  // to 18 key tiles long, 103 instead of 115 as one shared list.
+  const long long full = N <= THREADS ? 0 : N / G * G;
   int units_rest = 0, my_tiles = 0;
-  const int rest0 = static_cast<int>(N - full);   // < G <= THREADS
+  const int rest0 = static_cast<int>(N - full);   // <= THREADS (G is below it)
   if (static_cast<int>(threadIdx.x) < rest0) {
     int b, j;
     tile_at(first_tile, late_tile, B, N1, full + threadIdx.x, b, j);
@@ -366,10 +380,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int longest_in_warp = __reduce_max_sync(0xffffffffu, my_tiles);
   if (lane == 0 && longest_in_warp > 0) atomicMax(&ctrl->last, longest_in_warp);
   __syncthreads();
-  const bool share_rest = full == 0 || units_rest / G + 6 < ctrl->last;
+  const int shared_by = min(G, max(rest0, units_rest / 6));
+  const int longest = ctrl->last;
+  const int whole_rest = rest0 <= G ? longest : max(longest, units_rest / G + longest / 2);
+  const bool share_rest = rest0 > 0 && units_rest / shared_by + 6 < whole_rest;
   const long long W = share_rest ? full : N;
-  const int rest = share_rest ? rest0 : 0;
-  const int Gr = rest == 0 ? 0 : min(G, max(rest, units_rest / 6));
+  const int Gr = share_rest ? shared_by : 0;
   const bool shares = static_cast<int>(blockIdx.x) < Gr;
   const int u0 = shares ? static_cast<int>(static_cast<long long>(blockIdx.x) * units_rest / Gr) : 0;
   const int u1 = shares ? static_cast<int>(static_cast<long long>(blockIdx.x + 1) * units_rest / Gr) : 0;
@@ -468,10 +484,46 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
       ++sent;
-      if (C::INT4) return;   // 4-bit tiles: warps 2 and 3
       t1 = w.t1;
       const k8::Sight sight = w.t.sight;
       const int lo_tile = w.t.lo_tile, sink_tiles = w.t.sink_tiles;
+      if (C::INT4) {   // whole runs of rows and of their scale pairs, for warps 2 and 3 to unpack
+        for (int i = t0; i < t1 && ok; ++i) {
+          const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE + lane * bp;
+          int id = -1;   // of this lane's run
+          if (lane < TILE / bp && key < sight.len && (key + bp > sight.lo || key < sight.sinks)) id = kv_page(p.kv, b, key);
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * bp * (D / 2 + 4);
+          const int row = kv_row_in_page(p.kv, head, key);
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = warp_wait(&ctrl->raw_empty[slot], ph ^ 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
+            if (!ok) break;
+            if (withhold) {
+              withhold = false;
+            } else {
+              if (lane == 0) {
+                if (bytes) mbar_arrive_expect_tx(&ctrl->raw_full[slot], bytes);
+                else mbar_arrive(&ctrl->raw_full[slot]);
+              }
+              __syncwarp();
+              if (id >= 0) {
+                const uint32_t dst = smem_u32(raw) + slot * C::RAW_TILE;
+                k8::bulk_load_at(dst + lane * bp * (D / 2),
+                          (kv ? p.kv.v : p.kv.k) + id * p.kv.page_stride + static_cast<long long>(row) * (D / 2), bp * (D / 2),
+                          &ctrl->raw_full[slot]);
+                k8::bulk_load_at(dst + C::RAW_CODES + lane * bp * 4, (kv ? p.kv.v_scale : p.kv.k_scale) + id * p.kv.scale_stride + row,
+                          bp * 4, &ctrl->raw_full[slot]);
+              }
+              armed |= 1u << slot;
+              parity = (parity & ~(1u << slot)) | (ph << slot);
+            }
+            if (++slot == C::RAWS) {
+              slot = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        return;
+      }
       for (int i = t0; i < t1 && ok; ++i) {
         const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE + part * bp;
         int id = -1;
@@ -628,9 +680,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_OTHER));
     constexpr int CH = D / 8, STEP = 64 / CH;   // 16-byte chunks of a row; rows of one turn of the 64 threads
     const int t = threadIdx.x - 64, c = t % CH;
-    uint32_t pieces = 0, tiles = 0, ph = 0;
-    int slot = 0;
-    const bool withhold = prm.stall != 0 && blockIdx.x == 0;
+    uint32_t pieces = 0, tiles = 0, ph = 0, raw_ph = 0;
+    int slot = 0, raw_slot = 0;
     bool ok = true;
     while (ok) {
       const Piece* w = take();
@@ -652,101 +703,104 @@ __global__ void __launch_bounds__(THREADS, 1)
       const long long step = (static_cast<long long>(STEP % p.group) * p.kv.M + STEP / p.group) * D;
       const long long wrap = (1 - static_cast<long long>(p.group) * p.kv.M) * D;
       const uint32_t dst = smem_u32(smem) + (c >> 3) * C::HALF_BYTES;
-#pragma unroll 2
-      for (int k = 0; k < ROWS / 8; ++k) {
+      auto to = [&](int k, int e) {   // shared address of this thread's chunk of row k * 8 + e * STEP + row0
+        const int row = k * 8 + e * STEP + row0;
+        return dst + (row >= TILE ? C::TILE_BYTES - TILE * 128 : 0) + row * 128 + (((c & 7) ^ ((e * STEP + row0) & 7)) << 4);
+      };
+      auto advance = [&]() {
+        src += step;
+        hq += STEP % p.group;
+        if (hq >= p.group) {
+          hq -= p.group;
+          src += wrap;
+        }
+      };
+      if (C::INT4) {   // the d of every eight in the order in which codes come out of a word
+        constexpr int AT_ONCE = 16, PER = 8 / STEP;   // loads at a time; of one k
+#pragma unroll 1
+        for (int k = 0; k < ROWS / 8; k += AT_ONCE / PER) {
+          uint4 y[AT_ONCE];
 #pragma unroll
-        for (int e = 0; e < 8 / STEP; ++e) {
-          const int row = k * 8 + e * STEP + row0;
-          const bool in = r0 + row < rows;
-          k8::cp16(dst + (row >= TILE ? C::TILE_BYTES - TILE * 128 : 0) + row * 128 + (((c & 7) ^ ((e * STEP + row0) & 7)) << 4),
-                   in ? src : p.q, in ? 16 : 0);
-          src += step;
-          hq += STEP % p.group;
-          if (hq >= p.group) {
-            hq -= p.group;
-            src += wrap;
+          for (int e = 0; e < AT_ONCE; ++e) {
+            y[e] = r0 + k * 8 + e * STEP + row0 < rows ? ldg16(src) : make_uint4(0, 0, 0, 0);
+            advance();
+          }
+#pragma unroll
+          for (int e = 0; e < AT_ONCE; ++e)
+            st_shared_v4(to(k + e / PER, e % PER),
+                         make_uint4(__byte_perm(y[e].x, y[e].z, 0x5410), __byte_perm(y[e].x, y[e].z, 0x7632),
+                                    __byte_perm(y[e].y, y[e].w, 0x5410), __byte_perm(y[e].y, y[e].w, 0x7632)));
+        }
+      } else {
+#pragma unroll 2
+        for (int k = 0; k < ROWS / 8; ++k) {
+#pragma unroll
+          for (int e = 0; e < 8 / STEP; ++e) {
+            const bool in = r0 + k * 8 + e * STEP + row0 < rows;
+            k8::cp16(to(k, e), in ? src : p.q, in ? 16 : 0);
+            advance();
           }
         }
+        k8::cp_commit();
+        k8::cp_wait<0>();
       }
-      k8::cp_commit();
-      k8::cp_wait<0>();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->q_full);
       if (C::INT4) {   // the piece's key and value tiles, unpacked into the ring
+        // codes: 16 bytes (32 values) a load, D / 32 lanes a row
+        constexpr int LR = D / 32, PASS = 64 / LR;   // lanes of a row, rows of a load
+        const int lr = t % LR, row0 = t / LR;
         for (int i = t0; i < t1 && ok; ++i, ++tiles) {
           const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
           const int at = tiles % C::AFFINES;
           ok = warp_wait(&ctrl->a_empty[at], ((tiles / C::AFFINES) & 1u) ^ 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
-          if (!ok) break;
-          // pages of the tile's eight runs of 16 keys, looked up by lanes 0-7
-          int page = -1;
-          if (lane < TILE / 16) {
-            const int k = key + lane * 16;
-            if (k < sight.len && (k + 16 > sight.lo || k < sight.sinks)) page = kv_page(p.kv, piece_b, k);
-          }
-#pragma unroll 1
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            // scales: two keys a thread
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int c2 = 2 * t + e, k = key + c2;
-              const int id = __shfl_sync(0xffffffffu, page, c2 >> 4);
-              float sc = 0.f, off = 0.f;
-              if (id >= 0 && sight.any(k)) {
-                const uint32_t pair = __ldg((kv ? p.kv.v_scale : p.kv.k_scale) + id * p.kv.scale_stride + kv_row_in_page(p.kv, piece_head, k));
-                sc = kv_scale_of(pair);
-                off = fmaf(8.f, sc, kv_min_of(pair));
-                if (!kv) {   // the scores in base 2
-                  sc *= p.scale_log2;
-                  off *= p.scale_log2;
-                }
-              }
-              float* a = reinterpret_cast<float*>(affine + at * C::AFFINE_TILE + kv * (TILE * 8)) + t * 4;
-              a[e] = sc;
-              a[2 + e] = off;
-            }
-            ok = warp_wait(&ctrl->empty[slot], ph ^ 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = ok && warp_wait(&ctrl->raw_full[raw_slot], raw_ph, abortf, status, kStatusWaitFull, p.wait_ns) &&
+                 warp_wait(&ctrl->empty[slot], ph ^ 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
             if (!ok) break;
-            // codes: 16 bytes (32 values) a load, D / 32 lanes a row
-            constexpr int LR = D / 32, PASS = 64 / LR;   // lanes of a row, rows of a pass
-            const int lr = t % LR, row0 = t / LR;
-            const uint32_t dst = smem_u32(ring) + slot * C::TILE_BYTES + (lr >> 1) * C::HALF_BYTES;
-            const uint8_t* base = kv ? p.kv.v : p.kv.k;
-#pragma unroll 1
-            for (int r = 0; r < TILE; r += 4 * PASS) {
-              uint4 x[4];
-              uint32_t got = 0;
+            const uint32_t from = smem_u32(raw) + raw_slot * C::RAW_TILE;
+            {
+              uint32_t pair[2];
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(pair[0]), "=r"(pair[1]) : "r"(from + C::RAW_CODES + t * 8));
+              float v[4];   // scales, offsets
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int row = r + e * PASS + row0, k = key + row;
-                const int id = __shfl_sync(0xffffffffu, page, row >> 4);
-                x[e] = make_uint4(0, 0, 0, 0);
-                if (id >= 0 && sight.any(k)) {
-                  got |= 1u << e;
-                  x[e] = ldg16(base + id * p.kv.page_stride + static_cast<long long>(kv_row_in_page(p.kv, piece_head, k)) * (D / 2) + lr * 16);
-                }
+              for (int e = 0; e < 2; ++e) {
+                const bool seen = sight.any(key + 2 * t + e);   // (other slots may hold anything)
+                const float sc = seen ? kv_scale_of(pair[e]) : 0.f, lo = seen ? kv_min_of(pair[e]) : 0.f;
+                // the scores in base 2; keys enter the product as 128 + code, values as code - 8
+                v[e] = kv ? sc : sc * p.scale_log2;
+                v[2 + e] = kv ? fmaf(8.f, sc, lo) : fmaf(-128.f, sc, lo) * p.scale_log2;
               }
+              float4* a = reinterpret_cast<float4*>(affine + at * C::AFFINE_TILE + kv * (TILE * 8)) + t;
+              *a = make_float4(v[0], v[1], v[2], v[3]);
+            }
+            const uint32_t dst = smem_u32(ring) + slot * C::TILE_BYTES + (lr >> 1) * C::HALF_BYTES + row0 * 128;
+            uint4 x[TILE / PASS];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int row = r + e * PASS + row0;
-                const uint32_t words[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+            for (int e = 0; e < TILE / PASS; ++e) x[e] = ld_shared_v4(from + (e * 64 + t) * 16);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const uint32_t y = words[q];   // code - 8 of its eight codes, in order
-                  const uint32_t a = k8::code_pair8(y), b = k8::code_pair8(y >> 4), c = k8::code_pair8(y >> 8), d = k8::code_pair8(y >> 12);
-                  uint4 o = make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410), __byte_perm(a, b, 0x7632),
-                                       __byte_perm(c, d, 0x7632));
-                  if (!(got >> e & 1u)) o = make_uint4(0, 0, 0, 0);
-                  st_shared_v4(dst + row * 128 + (((((lr & 1) << 2) + q) ^ (row & 7)) << 4), o);
-                }
+            for (int e = 0; e < TILE / PASS; ++e) {
+              const uint32_t words[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {   // a word's codes in the order (0, 4), (1, 5), (2, 6), (3, 7)
+                const uint32_t y = words[q];
+                const uint4 o = kv ? make_uint4(k8::code_pair8(y), k8::code_pair8(y >> 4), k8::code_pair8(y >> 8), k8::code_pair8(y >> 12))
+                                   : make_uint4(k8::code_pair(y), k8::code_pair(y >> 4), k8::code_pair(y >> 8), k8::code_pair(y >> 12));
+                st_shared_v4(dst + e * PASS * 128 + (((((lr & 1) << 2) + q) ^ (row0 & 7)) << 4), o);
               }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               if (kv) mbar_arrive(&ctrl->a_full[at]);
-              if (!(withhold && tiles == 0 && kv == 0)) mbar_arrive(&ctrl->full[slot]);
+              mbar_arrive(&ctrl->full[slot]);
+              mbar_arrive(&ctrl->raw_empty[raw_slot]);
+            }
+            if (++raw_slot == C::RAWS) {
+              raw_slot = 0;
+              raw_ph ^= 1u;
             }
             if (++slot == C::STAGES) {
               slot = 0;
@@ -807,7 +861,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_ld_wait();
         const uint32_t at = (before + (i - t0)) % C::AFFINES;
         const uint32_t ak = smem_u32(affine) + at * C::AFFINE_TILE;
-        if (C::INT4) {   // s (q . (c - 8)) + (m + 8 s) sum(q), in base 2 already
+        if (C::INT4) {   // s (q . (128 + c)) + (m - 128 s) sum(q), in base 2 already
           ok = warp_wait(&ctrl->a_full[at], ((before + (i - t0)) / C::AFFINES) & 1u, abortf, status, kStatusWaitConv, p.wait_ns);
           if (!ok) break;
           const f32x2 qs2 = pk2(qsum, qsum);
@@ -922,7 +976,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 16; e += 8) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = o[e + k] * inv;
+          for (int k = 0; k < 8; ++k) f[C::INT4 ? (k >> 1) + 4 * (k & 1) : k] = o[e + k] * inv;   // (4-bit: a word's order of d)
           *reinterpret_cast<uint4*>(dst + c0 + e) = pack8(f);
         }
       };
@@ -1034,8 +1088,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_dealloc(tmem, TMEM_COLS);
   }
   if (warp == 0 && *abortf)   // after an abort nobody has waited for the copies in flight
-    for (int s = 0; s < C::STAGES; ++s)
-      if (ctrl->armed & (1u << s)) k8::drain_wait(&ctrl->full[s], (ctrl->armed_parity >> s) & 1);
+    for (int s = 0; s < (C::INT4 ? C::RAWS : C::STAGES); ++s)
+      if (ctrl->armed & (1u << s)) k8::drain_wait(C::INT4 ? &ctrl->raw_full[s] : &ctrl->full[s], (ctrl->armed_parity >> s) & 1);
   if (threadIdx.x == 0 && atomicAdd(prm.claim + 1, 1u) == gridDim.x - 1) prm.claim[0] = prm.claim[1] = 0;   // the last block
 }
 
