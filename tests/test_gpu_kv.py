@@ -613,3 +613,28 @@ def test_sequences_that_share_pages(handle, fmt, n):
     outs = [fnl.paged_attention(handle, cache, fnl.KVBatch(_cu([n, n]), _i32(c.lens), x, n), q)["out"] for x in (tab, shared)]
     handle.check()
     assert torch.equal(*outs)
+
+
+def test_a_wait_that_runs_out_over_4_bit_pages(cuda_device):
+    """The same for prompts over 4-bit pages, whose copies go through a ring of their own."""
+    h = fnl.Handle(0, wait_ns=50_000_000, debug_stall_calls=1)
+    c = Cache("int4", [300, 200], 2, 128, 64, seed=90)
+    cache, tab = _dev(c)
+    batch = fnl.KVBatch(_cu([300, 200]), _i32(c.lens), tab, 300)
+    q = torch.randn(4, 500, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    fnl.paged_attention(h, cache, batch, q)
+    with pytest.raises(fnl.FnlError, match="status"):
+        h.check()
+    _check_attention(h, c, [300, 200], 4)
+    h.close()
+
+
+@FMT
+@pytest.mark.parametrize("B,n,ctx", [(1, 40, 5000), (6, 33, 700), (80, 70, 90), (100, 65, 10)])
+def test_prompts_shared_or_whole(handle, fmt, B, n, ctx):
+    """One long key axis over every block; few tiles taken whole; between one and two
+    waves, and more tiles than the shared list holds."""
+    g = np.random.default_rng(95 + B)
+    new = [int(x) for x in g.integers(n // 2, n + 1, B)]
+    c = Cache(fmt, [x + int(y) for x, y in zip(new, g.integers(ctx // 2, ctx + 1, B))], 2, 64, 64, seed=96)
+    assert "tensor" in _check_attention(handle, c, new, 16 if B == 100 else 8)

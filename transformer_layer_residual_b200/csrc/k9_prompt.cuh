@@ -50,6 +50,12 @@
 // The codes of a word keep the order in which shifts and masks bring them out; Q's
 // rows are stored in that order of d and the result's are put back.
 //
+// There the softmax is the bound: a scale and an offset for every score and probability
+// take a key tile from 1.1 to 3 us, more than unpacking it (1.2 us at D = 64, 2 at 128).
+// Left out: codes fetched through registers ahead of their use (111 -> 124 us on five
+// prompts continued over 4-bit pages), scales as bf16 pairs in shared memory, half the
+// loads and twice the conversions (103 -> 121 us).
+//
 // Slots that no row of the piece sees are not copied (whole pages) or are zeroed
 // in V's tile before the product (rows), since 0 * NaN would reach the result;
 // their scores are replaced, not added to.
@@ -366,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // else about half of the longest after the even share. Against always sharing what
   // fills no wave, four chunks of 25 tokens and one prompt of 900 over 4-bit pages
   // (D = 128) took 30 and 49 us instead of 41 and 65; five prompts of 172 row tiles, up
-  // to 18 key tiles long, 103 instead of 115 as one shared list.
+  // to 18 key tiles long, 100 instead of 115 as one shared list.
   const long long full = N <= THREADS ? 0 : N / G * G;
   int units_rest = 0, my_tiles = 0;
   const int rest0 = static_cast<int>(N - full);   // <= THREADS (G is below it)
