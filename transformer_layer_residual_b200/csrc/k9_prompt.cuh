@@ -51,9 +51,12 @@
 // rows are stored in that order of d and the result's are put back.
 //
 // There the softmax is the bound: a scale and an offset for every score and probability
-// take a key tile from 1.1 to 3 us, more than unpacking it (1.2 us at D = 64, 2 at 128).
-// Left out: codes fetched through registers ahead of their use (111 -> 124 us on five
-// prompts continued over 4-bit pages), scales as bf16 pairs in shared memory, half the
+// take longer than the products and than unpacking (a key tile 1.2 us at D = 64, 2 at
+// 128). Its scores go back to TMEM adjusted, in loops over 32 of them: unrolled over the
+// tile, waiting for instructions was the largest stall (102 -> 82 us on five prompts
+// continued over 4-bit pages).
+// Left out: codes fetched through registers ahead of their use (111 -> 124 us on these
+// prompts), and, before those loops, scales as bf16 pairs in shared memory, half the
 // loads and twice the conversions (103 -> 121 us).
 //
 // Slots that no row of the piece sees are not copied (whole pages) or are zeroed
@@ -861,48 +864,76 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = warp_wait(&ctrl->s_full[s], done & 1u, abortf, status, kStatusWaitTmemFull, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
-        uint32_t x[TILE];
+        const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
+        // some row of the warp does not see some key
+        const bool edge = key + TILE - 1 > w0 || (p.window > 0 && key <= w1 - p.window && key + TILE > p.sinks);
+        const int hi = pos - key, lo = p.window > 0 ? hi - p.window : -1, sk = p.sinks - key;
+        auto mask = [&](uint32_t* y, int c0) {   // of 32 scores; bit c: key c0 + c is seen (at most hi; above lo, or below sk)
+          const uint32_t seen = ones_to(hi - c0) & (~ones_to(lo - c0) | ones_to(sk - 1 - c0));
 #pragma unroll
-        for (int c = 0; c < TILE; c += 32) tmem_ld32(ts + c, x + c);
-        tmem_ld_wait();
+          for (int c = 0; c < 32; ++c)
+            if (!(seen >> c & 1u)) y[c] = 0xff800000u;   // -inf
+        };
+        uint32_t x[TILE];   // bf16 pages: the row's scores
         const uint32_t at = (before + (i - t0)) % C::AFFINES;
         const uint32_t ak = smem_u32(affine) + at * C::AFFINE_TILE;
-        if (C::INT4) {   // s (q . (128 + c)) + (m - 128 s) sum(q), in base 2 already
+        float m;
+        if (C::INT4) {
+          // s (q . (128 + c)) + (m - 128 s) sum(q), in base 2 already. In loops over 32 scores, which go back to TMEM
+          // in between: unrolled over the tile, this code does not stay in the instruction cache
           ok = warp_wait(&ctrl->a_full[at], ((before + (i - t0)) / C::AFFINES) & 1u, abortf, status, kStatusWaitConv, p.wait_ns);
           if (!ok) break;
           const f32x2 qs2 = pk2(qsum, qsum);
+          m = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < TILE; c0 += 32) {
+            uint32_t y[32];
+            tmem_ld32(ts + c0, y);
+            tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < TILE; c += 2) {
-            const uint4 a = ld_shared_v4(ak + c * 8);
-            const f32x2 y = fma2(pk2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
-                                 pk2(__uint_as_float(a.x), __uint_as_float(a.y)),
-                                 mul2(pk2(__uint_as_float(a.z), __uint_as_float(a.w)), qs2));
-            float y0, y1;
-            unpk2(y, y0, y1);
-            x[c] = __float_as_uint(y0);
-            x[c + 1] = __float_as_uint(y1);
+            for (int c = 0; c < 32; c += 2) {
+              const uint4 a = ld_shared_v4(ak + (c0 + c) * 8);
+              const f32x2 z = fma2(pk2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])),
+                                   pk2(__uint_as_float(a.x), __uint_as_float(a.y)),
+                                   mul2(pk2(__uint_as_float(a.z), __uint_as_float(a.w)), qs2));
+              float y0, y1;
+              unpk2(z, y0, y1);
+              y[c] = __float_as_uint(y0);
+              y[c + 1] = __float_as_uint(y1);
+            }
+            if (edge) mask(y, c0);
+            float m2[2] = {m, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 32; c += 4)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) m2[e] = max3(m2[e], __uint_as_float(y[c + 2 * e]), __uint_as_float(y[c + 2 * e + 1]));
+            m = fmaxf(m2[0], m2[1]);
+#pragma unroll
+            for (int c = 0; c < 32; c += 16) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = y[c + e];
+              tmem_st16(ts + c0 + c, w);
+            }
           }
-        }
-        const int key = (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
-        // some row of the warp does not see some key
-        if (key + TILE - 1 > w0 || (p.window > 0 && key <= w1 - p.window && key + TILE > p.sinks)) {
-          const int hi = pos - key, lo = p.window > 0 ? hi - p.window : -1, sk = p.sinks - key;
+          tmem_st_wait();
+        } else {
 #pragma unroll
-          for (int c0 = 0; c0 < TILE; c0 += 32) {   // bit c: key c0 + c is seen (at most hi; above lo, or below sk)
-            const uint32_t seen = ones_to(hi - c0) & (~ones_to(lo - c0) | ones_to(sk - 1 - c0));
+          for (int c = 0; c < TILE; c += 32) tmem_ld32(ts + c, x + c);
+          tmem_ld_wait();
+          if (edge) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!(seen >> c & 1u)) x[c0 + c] = 0xff800000u;   // -inf
+            for (int c0 = 0; c0 < TILE; c0 += 32) mask(x + c0, c0);
           }
+          float m4[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) m4[c] = fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 4]));
+#pragma unroll
+          for (int c = 8; c < TILE; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + 4 + e]));
+          m = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * scale;
         }
-        float m4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) m4[c] = fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 4]));
-#pragma unroll
-        for (int c = 8; c < TILE; c += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + 4 + e]));
-        const float m = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * (C::INT4 ? 1.f : scale);
         if (__any_sync(0xffffffffu, m > top + GROWTH)) {
           const bool grow = m > top + GROWTH;
           const float f = grow && top != -INFINITY ? k8::ex2(top - m) : 1.f;
@@ -926,28 +957,44 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float base = top == -INFINITY ? 0.f : top;
         const f32x2 scale2 = pk2(scale, scale), base2 = pk2(-base, -base);
         f32x2 part2 = pk2(0.f, 0.f);
+        if (C::INT4) {
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            uint32_t y[32], w[16];
+            tmem_ld32(ts + h * 32, y);
+            tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t w[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const f32x2 z = pk2(__uint_as_float(x[h * 32 + 2 * c]), __uint_as_float(x[h * 32 + 2 * c + 1]));
-            f32x2 y = C::INT4 ? add2(z, base2) : fma2(z, scale2, base2);
-            float a, d;
-            unpk2(y, a, d);
-            a = k8::ex2(a);
-            d = k8::ex2(d);
-            y = pk2(a, d);
-            if (c & 1) part2 = add2(part2, y);
-            else sum2 = add2(sum2, y);
-            if (C::INT4) {   // p s goes to the product, p (m + 8 s) is added at the end
+            for (int c = 0; c < 16; ++c) {
+              float a, d;
+              unpk2(add2(pk2(__uint_as_float(y[2 * c]), __uint_as_float(y[2 * c + 1])), base2), a, d);
+              const f32x2 e = pk2(k8::ex2(a), k8::ex2(d));
+              if (c & 1) part2 = add2(part2, e);
+              else sum2 = add2(sum2, e);
+              // p s goes to the product, p (m + 8 s) is added at the end
               const uint4 v = ld_shared_v4(ak + TILE * 8 + (h * 32 + 2 * c) * 8);
-              corr2 = fma2(y, pk2(__uint_as_float(v.z), __uint_as_float(v.w)), corr2);
-              unpk2(mul2(y, pk2(__uint_as_float(v.x), __uint_as_float(v.y))), a, d);
+              corr2 = fma2(e, pk2(__uint_as_float(v.z), __uint_as_float(v.w)), corr2);
+              unpk2(mul2(e, pk2(__uint_as_float(v.x), __uint_as_float(v.y))), a, d);
+              w[c] = pack_bf16x2(a, d);
             }
-            w[c] = pack_bf16x2(a, d);
+            tmem_st16(ts + h * 16, w);   // (over scores that have been read)
           }
-          tmem_st16(ts + h * 16, w);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t w[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const f32x2 z = pk2(__uint_as_float(x[h * 32 + 2 * c]), __uint_as_float(x[h * 32 + 2 * c + 1]));
+              float a, d;
+              unpk2(fma2(z, scale2, base2), a, d);
+              a = k8::ex2(a);
+              d = k8::ex2(d);
+              if (c & 1) part2 = add2(part2, pk2(a, d));
+              else sum2 = add2(sum2, pk2(a, d));
+              w[c] = pack_bf16x2(a, d);
+            }
+            tmem_st16(ts + h * 16, w);
+          }
         }
         sum2 = add2(sum2, part2);
         tmem_st_wait();
