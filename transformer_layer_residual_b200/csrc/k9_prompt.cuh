@@ -56,8 +56,8 @@
 // tile, waiting for instructions was the largest stall (102 -> 82 us on five prompts
 // continued over 4-bit pages).
 // Left out: codes fetched through registers ahead of their use (111 -> 124 us on these
-// prompts), and, before those loops, scales as bf16 pairs in shared memory, half the
-// loads and twice the conversions (103 -> 121 us).
+// prompts), and scales as bf16 pairs in shared memory, half the loads and twice the
+// conversions (82 -> 91 us).
 //
 // Slots that no row of the piece sees are not copied (whole pages) or are zeroed
 // in V's tile before the product (rows), since 0 * NaN would reach the result;
