@@ -90,11 +90,11 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float lo, float 
   return __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x5410);
 }
 
-// Resident blocks of an SM: the loads of more of them hide the coding's time (13 prompts into 4-bit pages and read
-// back: 120 us with three, 115 with four); without it three are what the registers give (two: 402 -> 419 us on 64
-// prompts into bf16 pages).
+// 4-bit pages: four resident blocks an SM, whose loads hide the coding's time (13 prompts appended and read back:
+// 120 us with three, 115 with four). bf16 pages: the compiler's own choice of registers (0: no bound); held to three
+// blocks, 12 sequences of 330 to 1000 tokens took 33 instead of 30 us.
 template <int D, int FMT, bool INTERLEAVED>
-__global__ void __launch_bounds__(kKvThreads, FMT == kKvInt4 ? 4 : 3) k7_append(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kKvThreads, FMT == kKvInt4 ? 4 : 0) k7_append(const __grid_constant__ AppendParams p) {
   constexpr int LANES = D / 16;               // threads of one row
   constexpr int UNITS = kKvThreads / LANES;   // rows in flight per block
   // rows loaded before the first is used; coding makes the unrolled code of four too long for the

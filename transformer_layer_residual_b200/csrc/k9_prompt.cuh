@@ -698,7 +698,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok || w->t1 == 0) break;
       const int t0 = w->t0, t1 = w->t1, lo_tile = w->t.lo_tile, sink_tiles = w->t.sink_tiles;
       const k8::Sight sight = w->t.sight;
-      const int piece_head = w->head, piece_b = w->b;
       const int r0 = w->t.r0, rows = w->t.rows, first = w->t.first, head0 = w->head * p.group;
       release();
       if (pieces > 0) ok = warp_wait(&ctrl->q_empty, (pieces - 1) & 1u, abortf, status, kStatusWaitEmpty, p.wait_ns);
