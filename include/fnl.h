@@ -396,7 +396,8 @@ fnl_status fnl_kv_gather(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* c
  * those with j > pos(m) - window or j < sinks (first tokens that stay visible;
  * sinks need a window). A token that sees nothing gets 0. lse (nullable, fp32
  * [Hq, M]): log sum_j exp(scale q . k[j]), -inf where nothing is seen, for joining
- * with the attention over another cache. Scores, softmax and sums are fp32; the
+ * with the attention over another cache. NaN in a token's q, or a score of
+ * +infinity, gives NaN in that row of out and of lse, and nowhere else. Scores, softmax and sums are fp32; the
  * probabilities are rounded to bf16 for the product with v; 4-bit keys and values
  * are used unrounded. Slots of the cache that no token of the batch sees are not
  * read, whatever they hold; visible ones have to be finite.

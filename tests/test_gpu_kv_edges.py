@@ -1,0 +1,60 @@
+"""The paged key/value cache at the edges of what its entry points allow: NaN in q."""
+import numpy as np
+import pytest
+import torch
+
+from kv_cases import Cache
+from transformer_layer_residual_b200 import fnl
+
+pytestmark = pytest.mark.gpu
+
+FMT = pytest.mark.parametrize("fmt", ["bf16", "int4"])
+
+
+@pytest.fixture(scope="module")
+def handle(cuda_device):
+    h = fnl.Handle(0)
+    yield h
+    h.close()
+
+
+def _i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device="cuda")
+
+
+def _cu(new):
+    return _i32(np.concatenate([[0], np.cumsum(new)]))
+
+
+def _dev(c):
+    """(KVCache, table) of a CPU case on the GPU."""
+    return fnl.KVCache(*[None if x is None else x.cuda() for x in c.pages + c.scales]), c.table.cuda()
+
+
+@FMT
+@pytest.mark.parametrize("new,lens", [([1, 1], [70, 3000]), ([3, 2], [40, 3000]), ([40, 20], [60, 3000])])
+def test_nan_in_q_stays_in_its_row(handle, fmt, new, lens):
+    """A NaN in one head of one token gives NaN in that row's output and log-sum-exp, in
+    every form and where a head's keys are shared by blocks; all other rows keep their bits."""
+    Hq, Hkv, D = 8, 2, 64
+    c = Cache(fmt, lens, Hkv, D, 32, seed=3)
+    cache, tab = _dev(c)
+    M = sum(new)
+    batch = fnl.KVBatch(_cu(new), _i32(lens), tab, max(new))
+    q = torch.randn(Hq, M, D, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    bad = q.clone()
+    rows = [(1, 0), (6, M - 1), (3, new[0])]   # (head, token): of the first sequence, of the long one
+    for hq, m in rows:
+        bad[hq, m, 5] = float("nan")
+    got = []
+    for x in (q, bad):
+        lse = torch.full((Hq, M), 7.0, device="cuda")
+        out = fnl.paged_attention(handle, cache, batch, x, lse=lse)["out"]
+        got.append((out.view(M, Hq, D).cpu(), lse.cpu()))
+    handle.check()
+    hit = torch.zeros(M, Hq, dtype=torch.bool)
+    for hq, m in rows:
+        hit[m, hq] = True
+    assert torch.isfinite(got[0][0].float()).all() and torch.isfinite(got[0][1]).all()
+    assert torch.isnan(got[1][0][hit].float()).all() and torch.isnan(got[1][1].t()[hit]).all()
+    assert torch.equal(got[1][0][~hit], got[0][0][~hit]) and torch.equal(got[1][1].t()[~hit], got[0][1].t()[~hit])

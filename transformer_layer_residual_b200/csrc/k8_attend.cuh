@@ -37,7 +37,8 @@
 //
 // Keys that no row may see (behind the sequence's end, before the window) are
 // never read: their copies write zeros, so what such slots hold, NaN included,
-// cannot reach a result. A row that sees nothing gives 0 (log-sum-exp -inf).
+// cannot reach a result. A row that sees nothing gives 0 (log-sum-exp -inf); NaN in a
+// row's q or scores stays in that row and its log-sum-exp.
 #pragma once
 
 #include "kv_common.cuh"
@@ -563,14 +564,14 @@ template <int D, int N>
 __device__ __forceinline__ void store_row_part(const AttnParams& p, int first, int head, int r, int d0, const float (&v)[N],
                                                float top, float sum) {
   const int token = first + r / p.group, hq = head * p.group + r % p.group;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (a sum that is NaN stays one)
   bf16* dst = p.out + (static_cast<long long>(token) * p.Hq + hq) * D + d0;
 #pragma unroll
   for (int i = 0; i < N; i += 4)
     *reinterpret_cast<uint2*>(dst + i) =
         make_uint2(pack_bf16x2(v[i] * inv, v[i + 1] * inv), pack_bf16x2(v[i + 2] * inv, v[i + 3] * inv));
   if (d0 == 0 && p.lse)
-    p.lse[static_cast<long long>(hq) * p.kv.M + token] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    p.lse[static_cast<long long>(hq) * p.kv.M + token] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <int D, int FMT, int NR>

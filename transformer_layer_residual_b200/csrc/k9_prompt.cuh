@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       };
       auto put_lse = [&]() {
-        if (p.lse) p.lse[static_cast<long long>(hq) * p.kv.M + token] = sum > 0.f ? (top + log2f(sum)) * k8::kLn2 : -INFINITY;
+        if (p.lse) p.lse[static_cast<long long>(hq) * p.kv.M + token] = sum != 0.f ? (top + log2f(sum)) * k8::kLn2 : -INFINITY;
       };
       const bool whole = w->whole();
       const int c0 = w->c0, c1 = w->c1;
@@ -1049,12 +1049,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_ld16(to + d0, o);
             tmem_ld_wait();
           }
-          // (a row without keys, and a sub-tile without tiles, have no accumulators)
+          // (a row without keys, and a sub-tile without tiles, have no accumulators; a sum that is NaN stays one)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) f[e] = sum > 0.f ? __uint_as_float(o[e]) + (C::INT4 ? corr : 0.f) : 0.f;
+          for (int e = 0; e < 16; ++e) f[e] = sum != 0.f ? __uint_as_float(o[e]) + (C::INT4 ? corr : 0.f) : 0.f;
           if (r < rows) {
             if (whole) {
-              put(d0, f, sum > 0.f ? 1.f / sum : 0.f);
+              put(d0, f, sum != 0.f ? 1.f / sum : 0.f);
             } else {
 #pragma unroll
               for (int e = 0; e < 16; e += 4)
@@ -1122,7 +1122,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                   }
                 }
               }
-              put(d0, acc, sum > 0.f ? 1.f / sum : 0.f);
+              put(d0, acc, sum != 0.f ? 1.f / sum : 0.f);
             }
             put_lse();
           }
