@@ -344,8 +344,9 @@ typedef struct {
  * block_table[b * max_pages + t / page_size]. cu_q, kv_len and block_table are
  * DEVICE arrays that the kernels read when they run (a captured graph replays
  * with their new contents); max_q is the caller's bound on any sequence's new
- * tokens. Sequences without new tokens, and rows behind cu_q[B], are allowed: such
- * rows of the outputs are left as they were. Entries of block_table that no
+ * tokens. Sequences without new tokens (their kv_len and table entries are not used),
+ * and rows behind cu_q[B], are allowed: such rows of the outputs are left as they were.
+ * Entries of block_table that no
  * visible position needs are not read (pages that have left a window may be
  * reused).
  * The arrays' contents cannot be checked on the host: a page id outside

@@ -1,4 +1,5 @@
-"""The paged key/value cache at the edges of what its entry points allow: NaN in q."""
+"""The paged key/value cache at the edges of what its entry points allow: NaN in q, sequences
+without new tokens."""
 import numpy as np
 import pytest
 import torch
@@ -58,3 +59,26 @@ def test_nan_in_q_stays_in_its_row(handle, fmt, new, lens):
     assert torch.isfinite(got[0][0].float()).all() and torch.isfinite(got[0][1]).all()
     assert torch.isnan(got[1][0][hit].float()).all() and torch.isnan(got[1][1].t()[hit]).all()
     assert torch.equal(got[1][0][~hit], got[0][0][~hit]) and torch.equal(got[1][1].t()[~hit], got[0][1].t()[~hit])
+
+
+@FMT
+@pytest.mark.parametrize("n", [1, 30])
+@pytest.mark.parametrize("idle", [-1, 0, 1 << 30])
+def test_length_of_a_sequence_without_new_tokens_is_not_used(handle, fmt, n, idle):
+    """The free slots of a padded batch: whatever their kv_len, every call takes them alike."""
+    Hq, Hkv, D = 4, 2, 64
+    c = Cache(fmt, [50, 33], Hkv, D, 16, seed=5)
+    cache, tab = _dev(c)
+    table = torch.full((4, tab.shape[1]), -1, dtype=torch.int32, device="cuda")
+    table[0], table[2] = tab
+    g = torch.Generator().manual_seed(6)
+    q, k, v = (torch.randn(h, 2 * n, D, generator=g).to(torch.bfloat16).cuda() for h in (Hq, Hkv, Hkv))
+    got = []
+    for new, lens, t in (([n, n], [50, 33], tab), ([n, 0, n, 0], [50, idle, 33, idle], table)):
+        batch = fnl.KVBatch(_cu(new), _i32(lens), t, n)
+        fnl.rope_append_kv(handle, cache, batch, None, k, v)
+        out = fnl.paged_attention(handle, cache, batch, q)["out"]
+        back = fnl.kv_gather(handle, cache, batch, M=2 * n)
+        handle.check()
+        got.append((out, back["k"], back["v"]))
+    assert all(torch.equal(a, b) for a, b in zip(*got))

@@ -50,7 +50,8 @@ __device__ __forceinline__ KvSeq kv_seq(const KvParams& p, int b) {
   s.n = min(max(c1, s.first), p.M) - s.first;
   const long long room = static_cast<long long>(p.max_pages) << p.page_shift;
   s.len = static_cast<int>(min(static_cast<long long>(max(len, 0)), room));
-  if (c0 != s.first || c1 - c0 != s.n || s.n > p.max_q || len != s.len || len < s.n) kv_flag(p);
+  // (the length of a sequence without new tokens is not used)
+  if (c0 != s.first || c1 - c0 != s.n || (s.n > 0 && (s.n > p.max_q || len != s.len || len < s.n))) kv_flag(p);
   s.n = min(s.n, p.max_q);
   return s;
 }
