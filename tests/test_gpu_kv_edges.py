@@ -1,5 +1,5 @@
 """The paged key/value cache at the edges of what its entry points allow: NaN in q, sequences
-without new tokens."""
+without new tokens; and what a handle says of its calls."""
 import numpy as np
 import pytest
 import torch
@@ -82,3 +82,16 @@ def test_length_of_a_sequence_without_new_tokens_is_not_used(handle, fmt, n, idl
         handle.check()
         got.append((out, back["k"], back["v"]))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_last_plan_names_the_last_call(handle):
+    c = fnl.KVCache.empty(4, 16, 2, 64)
+    batch = fnl.KVBatch(_cu([3]), _i32([3]), _i32([2]).view(1, 1), 3)
+    q, k = (torch.randn(h, 3, 64, device="cuda").to(torch.bfloat16) for h in (4, 2))
+    fnl.rope_append_kv(handle, c, batch, None, k, k)
+    assert handle.last_plan() == "paged append, grid 3"
+    fnl.paged_attention(handle, c, batch, q)
+    assert "paged attention" in handle.last_plan()
+    fnl.kv_gather(handle, c, batch, M=3)
+    assert handle.last_plan() == "paged read-back, grid 3"
+    handle.check()

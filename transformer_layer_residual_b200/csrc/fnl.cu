@@ -1540,6 +1540,13 @@ fnl_status kv_launch(fnl_handle* h, Kern kern, dim3 grid, int threads, int smem,
   return FNL_OK;
 }
 
+// The plan's text (fnl_last_plan).
+void kv_plan(fnl_handle* h, const char* what, unsigned grid) {
+  char buf[160];
+  snprintf(buf, sizeof(buf), "%s, grid %u", what, grid);
+  h->plan_text = buf;
+}
+
 // Tokens per block: the most (a power of two, at most 8) that still leaves two
 // blocks for every SM, so that the angles of a token serve as many heads as
 // possible without idle SMs.
@@ -1610,9 +1617,7 @@ fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a
     --h->opt.debug_stall_calls;
   }
   if (a.kv.B > kMaxSeqs) return fail(h, FNL_ERR_UNSUPPORTED, "B=%d exceeds %d", a.kv.B, kMaxSeqs);
-  char buf[160];
-  snprintf(buf, sizeof(buf), "paged attention, tensor-core form, grid %d", h->num_sms);
-  h->plan_text = buf;
+  kv_plan(h, "paged attention, tensor-core form", static_cast<unsigned>(h->num_sms));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(h->num_sms));
   cfg.blockDim = dim3(THREADS);
@@ -1633,9 +1638,7 @@ fnl_status split_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p)
   typedef fnl::k8::SplitCfg<D, FMT, NR> C;
   static_assert(C::BLOCKS <= kKvBlocksPerSm, "workspace slots per SM");
   const int grid = h->num_sms * C::BLOCKS;
-  char buf[160];
-  snprintf(buf, sizeof(buf), "paged attention, split form, %d rows, grid %d", C::ROWS, grid);
-  h->plan_text = buf;
+  kv_plan(h, NR == 1 ? "paged attention, split form, 8 rows" : "paged attention, split form, 16 rows", static_cast<unsigned>(grid));
   return kv_launch(h, fnl::k8::k8_attend_split<D, FMT, NR>, dim3(grid), C::THREADS, C::SMEM, s, p);
 }
 
@@ -1684,6 +1687,7 @@ fnl_status fnl_rope_append_kv(fnl_handle* h, fnl_stream stream, const fnl_kv_cac
   p.cos = cos; p.sin = sin; p.Hq = Hq; p.rot = rot_dim; p.max_pos = max_pos;
   p.tokens = kv_tokens(h, M);
   const dim3 grid((M + p.tokens - 1) / p.tokens);
+  kv_plan(h, "paged append", grid.x);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool il = interleaved != 0, int4 = cache->format == FNL_KV_INT4;
   if (cache->D == 64)
@@ -1705,6 +1709,7 @@ fnl_status fnl_kv_gather(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* c
   p.k_out = Bm(k_out); p.v_out = Bm(v_out);
   p.tokens = kv_tokens(h, M);
   const dim3 grid((M + p.tokens - 1) / p.tokens);
+  kv_plan(h, "paged read-back", grid.x);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool int4 = cache->format == FNL_KV_INT4;
   if (cache->D == 64)
