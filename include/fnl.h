@@ -120,7 +120,8 @@ typedef struct {
   int max_tokens;   /* reserve workspace for M up to this (0: grow on demand) */
   int max_n;        /* reserve workspace for N up to this (0: grow on demand) */
   int path;         /* fnl_path */
-  int max_ctas;     /* cap on persistent CTAs (0: one per SM) -- for tests */
+  int max_ctas;     /* cap on persistent CTAs, of the GEMM and the paged attention kernels (0: as many as are
+                       resident) -- for tests */
   int precision;    /* fnl_precision */
   long long wait_ns;      /* limit of the kernels' main-loop waits in ns (0: 4 s). A wait that
                              runs out aborts its CTA and records a code for fnl_check. */

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from kv_cases import Cache
+from test_gpu_kv import _check_attention
 from transformer_layer_residual_b200 import fnl
 
 pytestmark = pytest.mark.gpu
@@ -95,3 +96,17 @@ def test_last_plan_names_the_last_call(handle):
     fnl.kv_gather(handle, c, batch, M=3)
     assert handle.last_plan() == "paged read-back, grid 3"
     handle.check()
+
+
+@FMT
+@pytest.mark.parametrize("ctas", [1, 3, 7])
+def test_capped_grids(cuda_device, fmt, ctas):
+    """max_ctas: long keys in few parts, many sequences and heads a block, more tiles than a block has threads."""
+    h = fnl.Handle(0, max_ctas=ctas)
+    c = Cache(fmt, [1500, 3, 700, 64], 2, 64, 32, seed=7)
+    for new, Hq, form in (([1, 1, 0, 1], 8, "8 rows"), ([3, 1, 2, 1], 8, "16 rows"), ([40, 3, 300, 0], 4, "tensor-core")):
+        plan = _check_attention(h, c, new, Hq, window=600, sinks=5)
+        assert form in plan and plan.endswith(f"grid {ctas}"), plan
+    c = Cache(fmt, [12] * 450, 1, 64, 16, seed=8)
+    assert _check_attention(h, c, [9] * 450, 2).endswith(f"grid {ctas}")
+    h.close()

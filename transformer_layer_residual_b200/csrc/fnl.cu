@@ -1547,6 +1547,11 @@ void kv_plan(fnl_handle* h, const char* what, unsigned grid) {
   h->plan_text = buf;
 }
 
+// Blocks of an attention kernel, whose work is dealt over however many there are.
+unsigned kv_grid(const fnl_handle* h, int resident) {
+  return static_cast<unsigned>(h->opt.max_ctas > 0 ? std::min(h->opt.max_ctas, resident) : resident);
+}
+
 // Tokens per block: the most (a power of two, at most 8) that still leaves two
 // blocks for every SM, so that the angles of a token serve as many heads as
 // possible without idle SMs.
@@ -1617,9 +1622,10 @@ fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a
     --h->opt.debug_stall_calls;
   }
   if (a.kv.B > kMaxSeqs) return fail(h, FNL_ERR_UNSUPPORTED, "B=%d exceeds %d", a.kv.B, kMaxSeqs);
-  kv_plan(h, "paged attention, tensor-core form", static_cast<unsigned>(h->num_sms));
+  const unsigned grid = kv_grid(h, h->num_sms);
+  kv_plan(h, "paged attention, tensor-core form", grid);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(h->num_sms));
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = Cfg<D, FMT>::SMEM;
   cfg.stream = s;
@@ -1637,8 +1643,8 @@ template <int D, int FMT, int NR>
 fnl_status split_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p) {
   typedef fnl::k8::SplitCfg<D, FMT, NR> C;
   static_assert(C::BLOCKS <= kKvBlocksPerSm, "workspace slots per SM");
-  const int grid = h->num_sms * C::BLOCKS;
-  kv_plan(h, NR == 1 ? "paged attention, split form, 8 rows" : "paged attention, split form, 16 rows", static_cast<unsigned>(grid));
+  const unsigned grid = kv_grid(h, h->num_sms * C::BLOCKS);
+  kv_plan(h, NR == 1 ? "paged attention, split form, 8 rows" : "paged attention, split form, 16 rows", grid);
   return kv_launch(h, fnl::k8::k8_attend_split<D, FMT, NR>, dim3(grid), C::THREADS, C::SMEM, s, p);
 }
 
