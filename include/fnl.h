@@ -128,7 +128,10 @@ typedef struct {
   int debug_stall_calls;  /* fault injection for tests of the status path: the next this-many
                              calls withhold one weight copy in their first CTA, so a wait for it
                              runs out after wait_ns (their outputs are then incomplete and
-                             fnl_check reports FNL_ERR_DEVICE_STATUS). 0 in normal use. */
+                             fnl_check reports FNL_ERR_DEVICE_STATUS). 0 in normal use. Paged
+                             attention withholds its first key copies; calls whose kernels have
+                             no bounded wait are not counted (paged append and read-back,
+                             attention of at most 16 rows over bf16 pages). */
   int tune;               /* 1: shape auto-tuning (TensorRT-LLM 深度工程实践, §2.4 内核自动调优:
                              candidate kernels run on the target GPU, the fastest is kept). With
                              path = FNL_PATH_AUTO, the first call of each shape (op, norm, N, K, and

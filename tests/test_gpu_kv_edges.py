@@ -1,5 +1,5 @@
 """The paged key/value cache at the edges of what its entry points allow: NaN in q, sequences
-without new tokens; and what a handle says of its calls."""
+without new tokens; a handle's options, and what it says of its calls."""
 import numpy as np
 import pytest
 import torch
@@ -109,4 +109,26 @@ def test_capped_grids(cuda_device, fmt, ctas):
         assert form in plan and plan.endswith(f"grid {ctas}"), plan
     c = Cache(fmt, [12] * 450, 1, 64, 16, seed=8)
     assert _check_attention(h, c, [9] * 450, 2).endswith(f"grid {ctas}")
+    h.close()
+
+
+@pytest.mark.parametrize("new", [[1, 1], [2, 1]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_wait_that_runs_out_in_the_split_form(cuda_device, D, new):
+    """Fault injection in a decode call over 4-bit pages: the block that withholds its first
+    copies ends, check() reports it, the next call on the handle is right. Calls without a
+    bounded wait leave the injection armed."""
+    h = fnl.Handle(0, wait_ns=50_000_000, debug_stall_calls=1)
+    wide = Cache("bf16", [300, 200], 1, D, 64, seed=50)
+    _check_attention(h, wide, new, 8)
+    c = Cache("int4", [3000, 200], 1, D, 64, seed=51)
+    cache, tab = _dev(c)
+    batch = fnl.KVBatch(_cu(new), _i32(c.lens), tab, max(new))
+    q = torch.randn(8, sum(new), D, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    fnl.kv_gather(h, cache, batch, M=sum(new))
+    fnl.paged_attention(h, cache, batch, q)
+    assert "split" in h.last_plan()
+    with pytest.raises(fnl.FnlError, match="status 1 "):
+        h.check()
+    _check_attention(h, c, new, 8)
     h.close()

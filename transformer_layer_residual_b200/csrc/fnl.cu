@@ -1552,6 +1552,13 @@ unsigned kv_grid(const fnl_handle* h, int resident) {
   return static_cast<unsigned>(h->opt.max_ctas > 0 ? std::min(h->opt.max_ctas, resident) : resident);
 }
 
+// Fault injection for the status-path tests: whether this call withholds its first copies.
+int kv_stall(fnl_handle* h) {
+  if (h->opt.debug_stall_calls <= 0) return 0;
+  --h->opt.debug_stall_calls;
+  return 1;
+}
+
 // Tokens per block: the most (a power of two, at most 8) that still leaves two
 // blocks for every SM, so that the angles of a token serve as many heads as
 // possible without idle SMs.
@@ -1597,6 +1604,7 @@ fnl_status page_map(fnl_handle* h, CUtensorMap* m, const KvParams& kv, const voi
 template <int D, int FMT>
 fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a) {
   using namespace fnl::k9;
+  if (a.kv.B > kMaxSeqs) return fail(h, FNL_ERR_UNSUPPORTED, "B=%d exceeds %d", a.kv.B, kMaxSeqs);
   fnl_status st = get_encoder(h);
   if (st != FNL_OK) return st;
   CUtensorMap mk, mv;
@@ -1617,11 +1625,7 @@ fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a
   Params p{};
   p.a = a;
   p.claim = reinterpret_cast<unsigned*>(h->kv_ws + kv_claim_offset(h));
-  if (h->opt.debug_stall_calls > 0) {   // fault injection for the status-path tests
-    p.stall = 1;
-    --h->opt.debug_stall_calls;
-  }
-  if (a.kv.B > kMaxSeqs) return fail(h, FNL_ERR_UNSUPPORTED, "B=%d exceeds %d", a.kv.B, kMaxSeqs);
+  p.a.stall = kv_stall(h);
   const unsigned grid = kv_grid(h, h->num_sms);
   kv_plan(h, "paged attention, tensor-core form", grid);
   cudaLaunchConfig_t cfg{};
@@ -1640,11 +1644,12 @@ fnl_status prompt_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& a
 }
 
 template <int D, int FMT, int NR>
-fnl_status split_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p) {
+fnl_status split_launch(fnl_handle* h, cudaStream_t s, fnl::AttnParams p) {
   typedef fnl::k8::SplitCfg<D, FMT, NR> C;
   static_assert(C::BLOCKS <= kKvBlocksPerSm, "workspace slots per SM");
   const unsigned grid = kv_grid(h, h->num_sms * C::BLOCKS);
   kv_plan(h, NR == 1 ? "paged attention, split form, 8 rows" : "paged attention, split form, 16 rows", grid);
+  if (C::BULK) p.stall = kv_stall(h);   // (the other form has no bounded wait)
   return kv_launch(h, fnl::k8::k8_attend_split<D, FMT, NR>, dim3(grid), C::THREADS, C::SMEM, s, p);
 }
 

@@ -56,6 +56,7 @@ struct AttnParams {
   unsigned long long wait_ns;   // limit of the waits for copies
   float* part;        // split form: [2 * blocks][kPartFloats]
   unsigned* counters; // split form: [blocks], zero between launches
+  int stall;          // fault injection for the status-path tests: block 0 withholds its first copies
 };
 
 namespace k8 {
@@ -675,9 +676,10 @@ __global__ void __launch_bounds__(SplitCfg<D, FMT, NR>::THREADS, SplitCfg<D, FMT
       return (i < st.sink_tiles ? i : st.lo_tile + i - st.sink_tiles) * C::TILE + warp * C::KEYS;
     };
     int page = -1;   // bulk form: this lane's page of the next step to copy
+    auto withheld = [&](uint32_t n) { return p.stall != 0 && n == 0 && warp == 0 && blockIdx.x == 0; };   // of step n
     auto issue = [&](int i) {
       const uint32_t slot = issued % C::STAGES;
-      bulk.issue(p.kv, head, key_of(i), page, ring + slot * L::kBytes, &full[warp][slot]);
+      if (!withheld(issued)) bulk.issue(p.kv, head, key_of(i), page, ring + slot * L::kBytes, &full[warp][slot]);
       ++issued;
       page = i + 1 < t1 ? bulk.page(p.kv, b, key_of(i + 1), sight) : -1;
     };
@@ -731,7 +733,8 @@ __global__ void __launch_bounds__(SplitCfg<D, FMT, NR>::THREADS, SplitCfg<D, FMT
     }
     if (C::BULK) {
       if (!ok)   // this warp's copies in flight land before the ring is used for anything else
-        for (; used != issued; ++used) drain_wait(&full[warp][used % C::STAGES], (used / C::STAGES) & 1);
+        for (; used != issued; ++used)
+          if (!withheld(used)) drain_wait(&full[warp][used % C::STAGES], (used / C::STAGES) & 1);
     } else {
       cp_wait<0>();
     }

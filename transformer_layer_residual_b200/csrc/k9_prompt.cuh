@@ -189,7 +189,6 @@ struct Cfg {
 struct Params {
   AttnParams a;
   unsigned* claim;   // whole tiles taken beyond the first wave; blocks that have ended. Both zero between launches
-  int stall;   // fault injection for the status-path tests: block 0 withholds its first key tile
 };
 
 // A row tile: 256 rows of a sequence (one key head) and its key tiles, the union
@@ -435,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int part = lane / C::HALVES, half = lane % C::HALVES;
     int slot = 0;
     uint32_t ph = 0, armed = 0, parity = 0;
-    bool withhold = prm.stall != 0 && blockIdx.x == 0;
+    bool withhold = p.stall != 0 && blockIdx.x == 0;
     bool ok = true;
     uint32_t sent = 0;
     // the last tile taken: its kind, head and sequence, row tiles of that kind before the sequence
