@@ -132,3 +132,45 @@ def test_a_wait_that_runs_out_in_the_split_form(cuda_device, D, new):
         h.check()
     _check_attention(h, c, new, 8)
     h.close()
+
+
+def test_a_handle_without_paged_calls_holds_no_cache_workspace(cuda_device):
+    """The workspace (39 MB on 148 SMs) comes with the first paged call, once, whether that
+    is eager or captured; a handle that makes none neither holds nor checks it."""
+    c = fnl.KVCache.empty(4, 16, 2, 64)
+    batch = fnl.KVBatch(_cu([3]), _i32([3]), _i32([2]).view(1, 1), 3)
+    q, k = (torch.randn(h, 3, 64, device="cuda").to(torch.bfloat16) for h in (4, 2))
+    out = torch.empty(3, 4 * 64, dtype=torch.bfloat16, device="cuda")
+
+    def calls(h):
+        fnl.rope_append_kv(h, c, batch, None, k, k)
+        fnl.paged_attention(h, c, batch, q, out=out)
+
+    h = fnl.Handle(0)
+    calls(h)           # (loads the kernels)
+    h.check()
+    h.close()
+    want = out.clone()
+    for captured in (False, True):
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        free = [torch.cuda.mem_get_info()[0]]
+        h = fnl.Handle(0)
+        h.check()
+        free.append(torch.cuda.mem_get_info()[0])
+        if captured:
+            side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                calls(h)
+            graph.replay()
+        else:
+            calls(h)
+        h.check()
+        free.append(torch.cuda.mem_get_info()[0])
+        calls(h)
+        h.check()
+        free.append(torch.cuda.mem_get_info()[0])
+        assert torch.equal(out, want)
+        h.close()
+        assert free[0] - free[1] < 8 << 20, free
+        assert free[1] - free[2] > 16 << 20 and free[2] == free[3], free

@@ -117,7 +117,7 @@ struct fnl_handle {
   int pairs = 0;             // resident CTA pairs of the pair kernel (0: not queried yet)
   std::vector<fnlh::TunedEntry> tuned;   // shape auto-tuning cache
   // Paged-cache calls: [status][arrival counters][partial sums], one fixed block
-  // that never moves (a captured graph keeps its addresses).
+  // that never moves (a captured graph keeps its addresses); null until the first call.
   uint8_t* kv_ws = nullptr;
   PageMaps page_maps;
 };
@@ -1141,7 +1141,7 @@ fnl_status fnl_create(fnl_handle** out, int device, const fnl_options* opt) {
     return FNL_ERR_INVALID_ARG;
   }
   h->device = device;
-  h->page_maps.e.reserve(PageMaps::kSize);   // (so that the paged-cache calls do not allocate)
+  h->page_maps.e.reserve(PageMaps::kSize);   // (so that neither grows in a call)
   h->plan_text.reserve(256);
   cudaError_t e = cudaSetDevice(device);
   if (e != cudaSuccess) {
@@ -1165,12 +1165,8 @@ fnl_status fnl_create(fnl_handle** out, int device, const fnl_options* opt) {
     need += align256(T * seg * fnl::k3::MAX_MPAD * 4) + align256(T * seg * fnl::k3::MAX_MPAD * 128 * 4);
   }
   fnl_status st = ensure_workspace(h, nullptr, need);
-  if (st == FNL_OK && (cudaMalloc(&h->kv_ws, kv_ws_bytes(h)) != cudaSuccess ||
-                       cudaMemset(h->kv_ws, 0, kv_fixed_bytes(h)) != cudaSuccess))
-    st = FNL_ERR_CUDA;
   if (st != FNL_OK) {
     if (h->ws) cudaFree(h->ws);
-    if (h->kv_ws) cudaFree(h->kv_ws);
     delete h;
     return st;
   }
@@ -1213,14 +1209,14 @@ fnl_status fnl_check(fnl_handle* h, fnl_stream stream) {
   int status = 0, kv_status = 0;
   e = cudaMemcpy(&status, h->ws, sizeof(int), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(h, e, "cudaMemcpy(status)");
-  e = cudaMemcpy(&kv_status, h->kv_ws, sizeof(int), cudaMemcpyDeviceToHost);
+  if (h->kv_ws) e = cudaMemcpy(&kv_status, h->kv_ws, sizeof(int), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(h, e, "cudaMemcpy(status of the paged-cache calls)");
   if (status != 0 || kv_status != 0) {
     // A CTA that gave up never made its split-K arrival, so its tiles' arrival
     // counters are left part-way; clear them with the status word, or every later
     // call would elect the wrong last CTA.
     e = cudaMemset(h->ws, 0, kFixedBytes);
-    if (e == cudaSuccess) e = cudaMemset(h->kv_ws, 0, kv_fixed_bytes(h));
+    if (e == cudaSuccess && h->kv_ws) e = cudaMemset(h->kv_ws, 0, kv_fixed_bytes(h));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(h, e, "cudaMemset(status, counters)");
     return fail(h, FNL_ERR_DEVICE_STATUS,
@@ -1404,6 +1400,28 @@ namespace {
 
 using fnl::KvParams;
 
+// The paged-cache block, allocated by the handle's first such call (most of it is the partial sums of 256-row
+// pieces, 39 MB on 148 SMs, which a handle that attends to nothing should not hold). That call may be inside a
+// stream capture: the allocation and its zeros are no part of the graph.
+fnl_status ensure_kv_ws(fnl_handle* h) {
+  if (h->kv_ws) return FNL_OK;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return cuda_fail(h, e, "cudaThreadExchangeStreamCaptureMode");
+  void* p = nullptr;
+  cudaStream_t s = nullptr;
+  e = cudaMalloc(&p, kv_ws_bytes(h));
+  if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, kv_fixed_bytes(h), s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (s) cudaStreamDestroy(s);
+  if (e != cudaSuccess && p) cudaFree(p);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return cuda_fail(h, e, "allocation of the paged-cache workspace");
+  h->kv_ws = static_cast<uint8_t*>(p);
+  return FNL_OK;
+}
+
 // Checks the cache and the batch and fills the kernels' parameters. `what` names
 // the outputs for messages only.
 fnl_status kv_params(fnl_handle* h, const fnl_kv_cache* c, const fnl_kv_batch* b, int M, KvParams* p) {
@@ -1459,10 +1477,11 @@ fnl_status kv_params(fnl_handle* h, const fnl_kv_cache* c, const fnl_kv_batch* b
   const void* p4[] = {b->cu_q, b->kv_len, b->block_table};
   for (const void* q : p4)
     if (!al4(q)) return fail(h, FNL_ERR_ALIGNMENT, "cu_q, kv_len and block_table must be 4-byte aligned");
-  p->status = reinterpret_cast<int*>(h->kv_ws);
   cudaError_t e = cudaSetDevice(h->device);
   if (e != cudaSuccess) return cuda_fail(h, e, "cudaSetDevice");
-  return FNL_OK;
+  fnl_status st = ensure_kv_ws(h);
+  p->status = reinterpret_cast<int*>(h->kv_ws);
+  return st;
 }
 
 // The caller's regions that a paged-cache call reads or writes. Pages may be
