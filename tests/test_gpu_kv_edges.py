@@ -1,5 +1,7 @@
 """The paged key/value cache at the edges of what its entry points allow: NaN in q, sequences
 without new tokens; a handle's options, and what it says of its calls."""
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -154,6 +156,8 @@ def test_a_handle_without_paged_calls_holds_no_cache_workspace(cuda_device):
     for captured in (False, True):
         out.fill_(7.0)
         torch.cuda.synchronize()
+        gc.collect()
+        torch.cuda.empty_cache()   # (as the start of a capture does)
         free = [torch.cuda.mem_get_info()[0]]
         h = fnl.Handle(0)
         h.check()
