@@ -191,27 +191,34 @@ __global__ void __launch_bounds__(kKvThreads, FMT == kKvInt4 ? 4 : 0) k7_append(
         if (live && page >= 0 && r >= p.Hq && r < rows) {
           const int h = is_v ? r - p.Hq - Hkv : r - p.Hq;
           const int row = (h << p.kv.page_shift) + row_in_page;
-          uint8_t* dst = (is_v ? p.kv.v : p.kv.k) + page * p.kv.page_stride + static_cast<long long>(row) * (D / 2);
-          *reinterpret_cast<uint32_t*>(dst + (e0 >> 1)) = codes8(a, lo, s, inv);
-          *reinterpret_cast<uint32_t*>(dst + (e1 >> 1)) = codes8(d, lo, s, inv);
-          if (c == 0)
-            (is_v ? p.kv.v_scale : p.kv.k_scale)[page * p.kv.scale_stride + row] =
-                (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
+          const long long page_rows = static_cast<long long>(Hkv) << p.kv.page_shift;
+          uint8_t* base = (is_v ? p.kv.v : p.kv.k) + page * p.kv.page_stride;
+          uint8_t* dst = base + static_cast<long long>(row) * (D / 2);
+          kv_store(p.kv, dst + (e0 >> 1), codes8(a, lo, s, inv), base, page_rows * (D / 2));
+          kv_store(p.kv, dst + (e1 >> 1), codes8(d, lo, s, inv), base, page_rows * (D / 2));
+          if (c == 0) {
+            uint32_t* pairs = (is_v ? p.kv.v_scale : p.kv.k_scale) + page * p.kv.scale_stride;
+            kv_store(p.kv, pairs + row, (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u), pairs, page_rows * 4);
+          }
         }
       }
       if (live && r < rows && (FMT == kKvBf16 || r < p.Hq)) {
         bf16* dst = nullptr;
+        const void* base = p.q_out;
+        long long size = static_cast<long long>(p.Hq) * M * (D * 2);
         if (r < p.Hq) {
           dst = p.q_out + (static_cast<long long>(r) * M + m) * D;
         } else if (page >= 0) {
           const int h = is_v ? r - p.Hq - Hkv : r - p.Hq;
           const int row = (h << p.kv.page_shift) + row_in_page;
-          dst = reinterpret_cast<bf16*>((is_v ? p.kv.v : p.kv.k) + page * p.kv.page_stride +
-                                        static_cast<long long>(row) * (D * 2));
+          uint8_t* to = (is_v ? p.kv.v : p.kv.k) + page * p.kv.page_stride;
+          dst = reinterpret_cast<bf16*>(to + static_cast<long long>(row) * (D * 2));
+          base = to;
+          size = (static_cast<long long>(Hkv) << p.kv.page_shift) * (D * 2);
         }
         if (dst) {
-          *reinterpret_cast<uint4*>(dst + e0) = x0[i];
-          *reinterpret_cast<uint4*>(dst + e1) = x1[i];
+          kv_store(p.kv, dst + e0, x0[i], base, size);
+          kv_store(p.kv, dst + e1, x1[i], base, size);
         }
       }
     }
@@ -270,9 +277,11 @@ __global__ void __launch_bounds__(kKvThreads) k7_gather(const __grid_constant__ 
       y0 = pack8(f0);
       y1 = pack8(f1);
     }
-    uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + (static_cast<long long>(h) * M + m) * D + c * 16);
-    dst[0] = y0;
-    dst[1] = y1;
+    bf16* out = is_v ? p.v_out : p.k_out;
+    bf16* dst = out + (static_cast<long long>(h) * M + m) * D + c * 16;
+    const long long size = static_cast<long long>(Hkv) * M * (D * 2);
+    kv_store(p.kv, dst, y0, out, size);
+    kv_store(p.kv, dst + 8, y1, out, size);
   }
 }
 

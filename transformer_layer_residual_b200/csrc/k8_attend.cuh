@@ -559,6 +559,11 @@ __device__ __forceinline__ long long q_row(const AttnParams& p, int first, int h
   return static_cast<long long>(hq) * p.kv.M + token;
 }
 
+__device__ __forceinline__ long long lse_bytes(const AttnParams& p) { return static_cast<long long>(p.Hq) * p.kv.M * 4; }
+__device__ __forceinline__ long long out_bytes(const AttnParams& p, int D) {
+  return static_cast<long long>(p.Hq) * p.kv.M * (2 * D);
+}
+
 // N consecutive values of row r from d0 on, divided by the row's sum; the lane
 // that holds d = 0 writes the log-sum-exp.
 template <int D, int N>
@@ -569,10 +574,11 @@ __device__ __forceinline__ void store_row_part(const AttnParams& p, int first, i
   bf16* dst = p.out + (static_cast<long long>(token) * p.Hq + hq) * D + d0;
 #pragma unroll
   for (int i = 0; i < N; i += 4)
-    *reinterpret_cast<uint2*>(dst + i) =
-        make_uint2(pack_bf16x2(v[i] * inv, v[i + 1] * inv), pack_bf16x2(v[i + 2] * inv, v[i + 3] * inv));
+    kv_store(p.kv, dst + i, make_uint2(pack_bf16x2(v[i] * inv, v[i + 1] * inv), pack_bf16x2(v[i + 2] * inv, v[i + 3] * inv)),
+             p.out, out_bytes(p, D));
   if (d0 == 0 && p.lse)
-    p.lse[static_cast<long long>(hq) * p.kv.M + token] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    kv_store(p.kv, p.lse + static_cast<long long>(hq) * p.kv.M + token, sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY,
+             p.lse, lse_bytes(p));
 }
 
 template <int D, int FMT, int NR>
@@ -788,11 +794,12 @@ __global__ void __launch_bounds__(SplitCfg<D, FMT, NR>::THREADS, SplitCfg<D, FMT
       if (works) {
 #pragma unroll
         for (int e = 0; e < PER; e += 4)
-          __stcg(reinterpret_cast<float4*>(mine + row * D + d0 + e), make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]));
+          kv_store_cg(p.kv, mine + row * D + d0 + e, make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]), mine,
+                      kPartFloats * 4);
       }
       if (works && d0 == 0) {
-        __stcg(mine + C::ROWS * D + row, top);
-        __stcg(mine + C::ROWS * D + C::ROWS + row, sum);
+        kv_store_cg(p.kv, mine + C::ROWS * D + row, top, mine, kPartFloats * 4);
+        kv_store_cg(p.kv, mine + C::ROWS * D + C::ROWS + row, sum, mine, kPartFloats * 4);
       }
       __threadfence();
       __syncthreads();

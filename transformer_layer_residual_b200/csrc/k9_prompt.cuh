@@ -1028,11 +1028,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int e = 0; e < 16; e += 8) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) f[C::INT4 ? (k >> 1) + 4 * (k & 1) : k] = o[e + k] * inv;   // (4-bit: a word's order of d)
-          *reinterpret_cast<uint4*>(dst + c0 + e) = pack8(f);
+          kv_store(p.kv, dst + c0 + e, pack8(f), p.out, k8::out_bytes(p, D));
         }
       };
       auto put_lse = [&]() {
-        if (p.lse) p.lse[static_cast<long long>(hq) * p.kv.M + token] = sum != 0.f ? (top + log2f(sum)) * k8::kLn2 : -INFINITY;
+        if (p.lse)
+          kv_store(p.kv, p.lse + static_cast<long long>(hq) * p.kv.M + token,
+                   sum != 0.f ? (top + log2f(sum)) * k8::kLn2 : -INFINITY, p.lse, k8::lse_bytes(p));
       };
       const bool whole = w->whole();
       const int c0 = w->c0, c1 = w->c1;
@@ -1057,8 +1059,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             } else {
 #pragma unroll
               for (int e = 0; e < 16; e += 4)
-                __stcg(reinterpret_cast<float4*>(mine_part) + ((d0 + e) >> 2) * ROWS + row,
-                       make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]));
+                kv_store_cg(p.kv, reinterpret_cast<float4*>(mine_part) + ((d0 + e) >> 2) * ROWS + row,
+                            make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]), mine_part, kPartFloats * 4);
             }
           }
         }
@@ -1066,8 +1068,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (whole) {
             put_lse();
           } else {
-            __stcg(mine_part + ROWS * D + row, top);
-            __stcg(mine_part + ROWS * D + ROWS + row, sum);
+            kv_store_cg(p.kv, mine_part + ROWS * D + row, top, mine_part, kPartFloats * 4);
+            kv_store_cg(p.kv, mine_part + ROWS * D + ROWS + row, sum, mine_part, kPartFloats * 4);
           }
         }
       }

@@ -75,6 +75,30 @@ __device__ __forceinline__ int kv_row_in_page(const KvParams& p, int head, int p
   return (head << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
 }
 
+// Stores of outputs, pages and partial sums. Debug builds (FNL_DEBUG_CHECKS) check each against the `size` bytes
+// from `base` on that it may write (of an output, a page, a slot): one outside is skipped and recorded as
+// kStatusBounds. Release builds compile the check away.
+__device__ __forceinline__ bool kv_in_bounds(const KvParams& p, const void* dst, int bytes, const void* base, long long size) {
+#ifdef FNL_DEBUG_CHECKS
+  const uint8_t* d = static_cast<const uint8_t*>(dst);
+  const uint8_t* b = static_cast<const uint8_t*>(base);
+  if (b == nullptr || d < b || d + bytes > b + size) {
+    atomicCAS(p.status, 0, kStatusBounds);
+    return false;
+  }
+#endif
+  return true;
+}
+template <typename T>
+__device__ __forceinline__ void kv_store(const KvParams& p, void* dst, const T& x, const void* base, long long size) {
+  if (kv_in_bounds(p, dst, sizeof(T), base, size)) *static_cast<T*>(dst) = x;
+}
+// The same past L1: other blocks read it.
+template <typename T>
+__device__ __forceinline__ void kv_store_cg(const KvParams& p, void* dst, const T& x, const void* base, long long size) {
+  if (kv_in_bounds(p, dst, sizeof(T), base, size)) __stcg(static_cast<T*>(dst), x);
+}
+
 __device__ __forceinline__ float kv_scale_of(uint32_t pair) { return bf_lo(pair); }
 __device__ __forceinline__ float kv_min_of(uint32_t pair) { return bf_hi(pair); }
 
