@@ -97,6 +97,11 @@ def test_last_plan_names_the_last_call(handle):
     assert "paged attention" in handle.last_plan()
     fnl.kv_gather(handle, c, batch, M=3)
     assert handle.last_plan() == "paged read-back, grid 3"
+    x, W = (torch.zeros(n, 64, dtype=torch.bfloat16, device="cuda") for n in (3, 64))
+    fnl.linear_add_residual(handle, x, W, x)
+    assert "paged" not in handle.last_plan() and handle.last_plan()
+    fnl.rope_append_kv(handle, c, batch, None, k, k)
+    assert handle.last_plan() == "paged append, grid 3"
     handle.check()
 
 
