@@ -183,3 +183,29 @@ def test_a_handle_without_paged_calls_holds_no_cache_workspace(cuda_device):
         h.close()
         assert free[0] - free[1] < 8 << 20, free
         assert free[1] - free[2] > 16 << 20 and free[2] == free[3], free
+
+
+@FMT
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("window,sinks", [(40, 4), (700, 500), (40, 500), (700, 4)])
+def test_from_the_sinks_to_a_far_window(handle, fmt, D, page, window, sinks):
+    """The keys between the sinks and the window take up whole tiles in every form (of 8 rows, of
+    16, of prompts), and the table has no page there."""
+    lens = [5001, 1, 3000]
+    c = Cache(fmt, lens, 2, D, page, seed=window + sinks)
+    for new, Hq, form in (([1, 1, 1], 16, "8 rows"), ([2, 1, 2], 16, "16 rows"), ([3, 0, 4], 4, "8 rows"), ([40, 1, 70], 6, "tensor")):
+        table = c.table.clone()
+        for b, n in enumerate(lens):
+            for i in range(table.shape[1]):
+                if i * page >= sinks and (i + 1) * page <= n - new[b] + 1 - window:
+                    table[b, i] = 1 << 30
+        assert form in _check_attention(handle, c, new, Hq, window, sinks, table=table)
+
+
+@FMT
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_heads_of_16_rows_over_many_blocks(handle, fmt, D):
+    """Two key heads over every block: dozens of parts of 16 rows added, and one of a few."""
+    c = Cache(fmt, [40001, 700], 1, D, 128, seed=100 + D)
+    for new, Hq in (([1, 1], 16), ([2, 1], 8), ([2, 0], 7)):
+        assert "16 rows" in _check_attention(handle, c, new, Hq)
