@@ -1412,23 +1412,20 @@ namespace {
 using fnl::KvParams;
 
 // The paged-cache block, allocated by the handle's first such call (most of it is the partial sums of 256-row
-// pieces, 39 MB on 148 SMs, which a handle that attends to nothing should not hold). Its zeros are written on that
-// call's stream; where this is being captured, the zeros, no part of the graph, take a stream of their own.
-fnl_status ensure_kv_ws(fnl_handle* h, cudaStream_t stream) {
+// pieces, 39 MB on 148 SMs, which a handle that attends to nothing should not hold). That call may be inside a
+// stream capture: the allocation and its zeros are no part of the graph.
+fnl_status ensure_kv_ws(fnl_handle* h) {
   if (h->kv_ws) return FNL_OK;
   cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
   cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
   if (e != cudaSuccess) return cuda_fail(h, e, "cudaThreadExchangeStreamCaptureMode");
   void* p = nullptr;
-  cudaStream_t own = nullptr;
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  e = cudaStreamIsCapturing(stream, &cap);
-  const bool captured = cap != cudaStreamCaptureStatusNone;
-  if (e == cudaSuccess) e = cudaMalloc(&p, kv_ws_bytes(h));
-  if (e == cudaSuccess && captured) e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
-  if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, kv_fixed_bytes(h), captured ? own : stream);
-  if (e == cudaSuccess && captured) e = cudaStreamSynchronize(own);
-  if (own) cudaStreamDestroy(own);
+  cudaStream_t s = nullptr;
+  e = cudaMalloc(&p, kv_ws_bytes(h));
+  if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, kv_fixed_bytes(h), s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (s) cudaStreamDestroy(s);
   if (e != cudaSuccess && p) cudaFree(p);
   cudaThreadExchangeStreamCaptureMode(&mode);
   if (e != cudaSuccess) return cuda_fail(h, e, "allocation of the paged-cache workspace");
@@ -1438,7 +1435,7 @@ fnl_status ensure_kv_ws(fnl_handle* h, cudaStream_t stream) {
 
 // Checks the cache and the batch and fills the kernels' parameters. `what` names
 // the outputs for messages only.
-fnl_status kv_params(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* c, const fnl_kv_batch* b, int M, KvParams* p) {
+fnl_status kv_params(fnl_handle* h, const fnl_kv_cache* c, const fnl_kv_batch* b, int M, KvParams* p) {
   if (!h) return FNL_ERR_INVALID_ARG;
   if (!c || !b) return fail(h, FNL_ERR_INVALID_ARG, "cache and batch are required");
   if (c->format != FNL_KV_BF16 && c->format != FNL_KV_INT4)
@@ -1493,7 +1490,7 @@ fnl_status kv_params(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* c, co
     if (!al4(q)) return fail(h, FNL_ERR_ALIGNMENT, "cu_q, kv_len and block_table must be 4-byte aligned");
   cudaError_t e = cudaSetDevice(h->device);
   if (e != cudaSuccess) return cuda_fail(h, e, "cudaSetDevice");
-  fnl_status st = ensure_kv_ws(h, reinterpret_cast<cudaStream_t>(stream));
+  fnl_status st = ensure_kv_ws(h);
   p->status = reinterpret_cast<int*>(h->kv_ws);
   return st;
 }
@@ -1701,7 +1698,7 @@ fnl_status fnl_rope_append_kv(fnl_handle* h, fnl_stream stream, const fnl_kv_cac
                               int M, int Hq, const fnl_bf16* q, const fnl_bf16* k, const fnl_bf16* v, const float* cos,
                               const float* sin, int rot_dim, int max_pos, int interleaved, fnl_bf16* q_out) {
   fnl::AppendParams p{};
-  fnl_status st = kv_params(h, stream, cache, batch, M, &p.kv);
+  fnl_status st = kv_params(h, cache, batch, M, &p.kv);
   if (st != FNL_OK) return st;
   if (rot_dim < 0 || rot_dim % 16 || rot_dim > cache->D)
     return fail(h, FNL_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [0, D] (rot_dim=%d)", rot_dim);
@@ -1741,7 +1738,7 @@ fnl_status fnl_rope_append_kv(fnl_handle* h, fnl_stream stream, const fnl_kv_cac
 fnl_status fnl_kv_gather(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* cache, const fnl_kv_batch* batch, int M,
                          fnl_bf16* k_out, fnl_bf16* v_out) {
   fnl::GatherParams p{};
-  fnl_status st = kv_params(h, stream, cache, batch, M, &p.kv);
+  fnl_status st = kv_params(h, cache, batch, M, &p.kv);
   if (st != FNL_OK || M == 0 || batch->B == 0) return st;
   if (!k_out || !v_out) return fail(h, FNL_ERR_INVALID_ARG, "k_out and v_out are required");
   if (!al16(k_out) || !al16(v_out)) return fail(h, FNL_ERR_ALIGNMENT, "k_out and v_out must be 16-byte aligned");
@@ -1766,7 +1763,7 @@ fnl_status fnl_paged_attention(fnl_handle* h, fnl_stream stream, const fnl_kv_ca
                                int M, int Hq, const fnl_bf16* q, float scale, int window, int sinks, fnl_bf16* out,
                                float* lse) {
   fnl::AttnParams p{};
-  fnl_status st = kv_params(h, stream, cache, batch, M, &p.kv);
+  fnl_status st = kv_params(h, cache, batch, M, &p.kv);
   if (st != FNL_OK) return st;
   if (Hq <= 0 || Hq > (1 << 20) || Hq % cache->Hkv)
     return fail(h, FNL_ERR_INVALID_ARG, "Hq (%d) must be a positive multiple of Hkv (%d), at most 2^20", Hq, cache->Hkv);
