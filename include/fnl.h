@@ -168,10 +168,12 @@ const char* fnl_last_plan(const fnl_handle* h);
  * (device codes 1-7) or, in the debug build libfnl_debug.so (compiled with
  * FNL_DEBUG_CHECKS), skipped an output store that would have left its buffer
  * (device code 8), or a paged-cache call met a batch description that does not
- * fit its cache (device code 9, see fnl_kv_batch); fnl_last_error() names the code. The outputs of the calls
- * since the last check are then not to be trusted. It
- * also resets the handle's split-K arrival counters (an aborted CTA leaves its
- * tiles' counters part-way), so later calls on the handle compute correctly. */
+ * fit its cache (device code 9, see fnl_kv_batch); fnl_last_error() names the
+ * code. The outputs of the calls since the last check are then not to be trusted.
+ * It also resets the handle's arrival counters, split-K and paged (an aborted CTA
+ * leaves its tiles' counters part-way), so later calls on the handle compute
+ * correctly. A handle that has made paged-cache calls has a second status word,
+ * read by a second blocking copy. */
 fnl_status fnl_check(fnl_handle* h, fnl_stream stream);
 
 /* Residual add -> norm -> QKV projection -> head-major GQA split.
@@ -403,10 +405,11 @@ fnl_status fnl_kv_gather(fnl_handle* h, fnl_stream stream, const fnl_kv_cache* c
  * sinks need a window). A token that sees nothing gets 0. lse (nullable, fp32
  * [Hq, M]): log sum_j exp(scale q . k[j]), -inf where nothing is seen, for joining
  * with the attention over another cache. NaN in a token's q, or a score of
- * +infinity, gives NaN in that row of out and of lse, and nowhere else. Scores, softmax and sums are fp32; the
- * probabilities are rounded to bf16 for the product with v; 4-bit keys and values
- * are used unrounded. Slots of the cache that no token of the batch sees are not
- * read, whatever they hold; visible ones have to be finite.
+ * +infinity, gives NaN in that row of out and of lse, and nowhere else. Scores,
+ * softmax and sums are fp32; the probabilities are rounded to bf16 for the product
+ * with v; 4-bit keys and values are used unrounded. Slots of the cache that no token
+ * of the batch sees do not reach a result, whatever they hold; those that share a
+ * page with a seen slot may be read. Visible slots have to be finite.
  * Any mix of lengths is correct; a batch of few new tokens per sequence (at most
  * 16 rows max_q * Hq / Hkv) runs the form that splits the keys over the whole GPU,
  * so decode steps and prompts are best given as two calls. Limits

@@ -1433,8 +1433,7 @@ fnl_status ensure_kv_ws(fnl_handle* h) {
   return FNL_OK;
 }
 
-// Checks the cache and the batch and fills the kernels' parameters. `what` names
-// the outputs for messages only.
+// Checks the cache and the batch and fills the kernels' parameters.
 fnl_status kv_params(fnl_handle* h, const fnl_kv_cache* c, const fnl_kv_batch* b, int M, KvParams* p) {
   if (!h) return FNL_ERR_INVALID_ARG;
   if (!c || !b) return fail(h, FNL_ERR_INVALID_ARG, "cache and batch are required");
@@ -1682,6 +1681,14 @@ fnl_status split_launch(fnl_handle* h, cudaStream_t s, fnl::AttnParams p) {
   return kv_launch(h, fnl::k8::k8_attend_split<D, FMT, NR>, dim3(grid), C::THREADS, C::SMEM, s, p);
 }
 
+// The split form holds up to 16 rows of a key head in a warp's registers, the tensor-core form tiles of 256. Where
+// both can run, the split form is faster. us, split / tensor-core, 8 key heads of D = 128:
+//   32 sequences of 4000   4 rows  8 rows   16 rows       64 sequences of 300   4 rows  8 rows  16 rows
+//     bf16                 89/128  90/128   92/128                              27/44   27/45   36/44
+//     4-bit                55/229  58/224   78/226                              19/65   22/65   46/65
+// (D = 64: 51/118 to 53/111 and 34/168 to 49/168; 17/37 to 21/37 and 12/54 to 25/54.) From 17 rows on the
+// tensor-core form takes the same time up to 64. Over long 4-bit sequences two calls of 16 rows would still take less
+// (156 against 227 us at the 4000), over short ones more (92 against 65).
 template <int D, int FMT>
 fnl_status attend_launch(fnl_handle* h, cudaStream_t s, const fnl::AttnParams& p) {
   const long long rows = static_cast<long long>(p.kv.max_q) * p.group;

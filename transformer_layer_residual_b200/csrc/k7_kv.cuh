@@ -90,15 +90,17 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float lo, float 
   return __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x5410);
 }
 
-// 4-bit pages: four resident blocks an SM, whose loads hide the coding's time (13 prompts appended and read back:
-// 120 us with three, 115 with four). bf16 pages: the compiler's own choice of registers (0: no bound); held to three
+// 4-bit pages: four resident blocks an SM, which hide more of the wait for loads (the first stall; issue slots 63 %
+// used, DRAM 51 %) although the bound of 64 registers spills 28 bytes a thread (13 prompts appended and read back:
+// 120 us with three, 115 with four; 88 + 24 us apart, their bytes 60 + 14). bf16 pages: the compiler's own choice of registers (0: no bound); held to three
 // blocks, 12 sequences of 330 to 1000 tokens took 33 instead of 30 us.
 template <int D, int FMT, bool INTERLEAVED>
 __global__ void __launch_bounds__(kKvThreads, FMT == kKvInt4 ? 4 : 0) k7_append(const __grid_constant__ AppendParams p) {
   constexpr int LANES = D / 16;               // threads of one row
   constexpr int UNITS = kKvThreads / LANES;   // rows in flight per block
   // rows loaded before the first is used; coding makes the unrolled code of four too long for the
-  // instruction cache (13 prompts appended to 4-bit pages and read back: 122 us with four, 120 with two)
+  // instruction cache (13 prompts appended to 4-bit pages and read back, three blocks an SM: 122 us with four, 120
+  // with two). The q rows, which are not coded, go in the same loop.
   constexpr int kRows = FMT == kKvInt4 ? 2 : 4;
   pdl_wait();
   const int T = p.tokens;

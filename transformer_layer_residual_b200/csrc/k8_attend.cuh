@@ -35,9 +35,10 @@
 // 2^-8 at most each, the same size as the output's own rounding); their sum is
 // taken in fp32 before that rounding.
 //
-// Keys that no row may see (behind the sequence's end, before the window) are
-// never read: their copies write zeros, so what such slots hold, NaN included,
-// cannot reach a result. A row that sees nothing gives 0 (log-sum-exp -inf); NaN in a
+// Keys that no row may see (behind the sequence's end, before the window) cannot
+// reach a result, whatever their slots hold, NaN included. Of bf16 pages they are
+// never read: their copies write zeros. Of 4-bit pages whole runs of up to 64 rows
+// of a page are copied; their scores are replaced and their scales taken as zeros. A row that sees nothing gives 0 (log-sum-exp -inf); NaN in a
 // row's q or scores stays in that row and its log-sum-exp.
 #pragma once
 
@@ -54,8 +55,8 @@ struct AttnParams {
   float scale_log2;   // scale * log2(e)
   int window, sinks;  // window 0: none
   unsigned long long wait_ns;   // limit of the waits for copies
-  float* part;        // split form: [2 * blocks][kPartFloats]
-  unsigned* counters; // split form: [blocks], zero between launches
+  float* part;        // partial sums: two slots a block, each of the form's own kPartFloats
+  unsigned* counters; // arrivals at a shared piece: one a block, zero between launches
   int stall;          // fault injection for the status-path tests: block 0 withholds its first copies
 };
 
@@ -467,11 +468,12 @@ struct SplitCfg {
   static constexpr int ROWS = NR * 8;                          // rows of a piece
   // keys of a warp's step, warps, steps in the ring, resident blocks of an SM: chosen
   // by measurement. bf16 pages are bound by memory: 192 KB of ring, two thirds of it
-  // in flight. 4-bit pages are bound by unpacking: 64-key steps (fewer loop and copy
+  // in flight. 4-bit pages take longer to unpack than to read (64 sequences of 2000 to
+  // 12000: issue slots 50 % used, DRAM 42 %): 64-key steps (fewer loop and copy
   // instructions) with as many warps as their registers leave, two blocks of 6 for 8
-  // rows (64 sequences of 2000 to 12000: 138 us; 32-key steps with 16 warps 150, with
+  // rows (those 64 sequences: 136 us; 32-key steps with 16 warps 150, with
   // 8 warps 181), one of 8 for 16 rows, whose state is twice as large (130003 keys:
-  // 68 us; two blocks of 6 98, 32-key steps with 12 warps 83).
+  // 67 us; two blocks of 6 98, 32-key steps with 12 warps 83).
   static constexpr int KEYS = FMT == kKvBf16 ? 32 : 64;
   static constexpr int WARPS = FMT == kKvBf16 ? 4 : (NR == 1 ? 6 : 8);
   static constexpr int STAGES = FMT == kKvBf16 ? 3 : 2;

@@ -50,11 +50,14 @@
 // The codes of a word keep the order in which shifts and masks bring them out; Q's
 // rows are stored in that order of d and the result's are put back.
 //
-// There the softmax is the bound: a scale and an offset for every score and probability
-// take longer than the products and than unpacking (a key tile 1.2 us at D = 64, 2 at
-// 128). Its scores go back to TMEM adjusted, in loops over 32 of them: unrolled over the
-// tile, waiting for instructions was the largest stall (102 -> 82 us on five prompts
-// continued over 4-bit pages).
+// There the softmax, with a scale and an offset for every score and probability, takes
+// longer than the products and than unpacking, which alone takes 1.2 us a key tile at
+// D = 64 and 2 us at 128. It is time spent waiting, not issue slots: these are used to
+// 32 % and the tensor pipe to 11 % (five prompts of 100 to 900 tokens continued over
+// 4-bit pages, D = 64, 81 us). Two of the softmax's warps share a scheduler, and a new
+// piece's tiles are unpacked only once its Q is in, which waits for the last piece's
+// products. The scores go back to TMEM adjusted, in loops over 32 of them: unrolled over
+// the tile, waiting for instructions was the largest stall (102 -> 82 us).
 // Left out: codes fetched through registers ahead of their use (111 -> 124 us on these
 // prompts), and scales as bf16 pairs in shared memory, half the loads and twice the
 // conversions (82 -> 91 us).
