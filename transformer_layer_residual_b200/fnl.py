@@ -113,11 +113,12 @@ class Handle:
     (small-M kernel, cluster form), "tile" (128x256 tiles), "wide" (128x512
     tiles), "pair" (256x512 tiles on CTA pairs), "pair_sk" (the pair kernel's
     stream-K form, its split tiles finished by the fix-up kernel). max_ctas
-    caps the grid (0 = all SMs). precision: "default" (split
+    caps the persistent grids (0 = all SMs). precision: "default" (split
     hi + lo operand for SwiGLU only), "split", "single". wait_ns: limit of the
     kernels' main-loop waits (0 = 4 s). debug_stall_calls: fault injection for
     tests of the status path (the next that-many calls withhold one weight copy,
-    so a wait runs out and check() raises). tune: shape auto-tuning (the first
+    or their first key copies, so a wait runs out and check() raises; calls without
+    a bounded wait are not counted, see fnl.h). tune: shape auto-tuning (the first
     call of each shape times the candidate plans and keeps the fastest)."""
 
     def __init__(self, device: int = 0, max_tokens: int = 0, max_n: int = 0, path: str = "auto",
